@@ -4,8 +4,8 @@ eviction) and the attention weight that a prompt's keys receive.
 `own` false: every operator in elementary torch operations, fp32.  `own` true: the package's entry points.
 `exact` computes the same from the definitions in 64 bits.
 
-Cache layout: pages of 64 slots; K codes [page, H_kv, 64, D], V codes [page, H_kv, D, 64], one fp32 scale per
-(page, head) for each; value = code * scale.  Scales are powers of two, so the codes (int8: whole numbers;
+Cache layout: pages of 64 slots; K and V codes [page, H_kv, 64, D], one fp32 scale per (page, head) for each;
+value = code * scale.  Scales are powers of two, so the codes (int8: whole numbers;
 e4m3: 8-bit floats) are the same in 32 and in 64 bits, and come back as the numbers they are, next to their scales.
 """
 import math
@@ -181,13 +181,13 @@ def _pools(g, case, n_pages, filled=True):
     if not filled:
         t = torch.int8 if code == "int8" else torch.float8_e4m3fn
         z = lambda *s: torch.zeros(s, dtype=torch.uint8, device=DEV).view(t)  # noqa: E731
-        return dict(k_codes=z(n_pages, H_kv, PAGE, D), v_codes=z(n_pages, H_kv, D, PAGE),
+        return dict(k_codes=z(n_pages, H_kv, PAGE, D), v_codes=z(n_pages, H_kv, PAGE, D),
                     k_scale=torch.zeros(n_pages, H_kv, device=DEV), v_scale=torch.zeros(n_pages, H_kv, device=DEV))
     k = _normal(g, n_pages, H_kv, PAGE, D)
     k *= 1.0 + 2.0 * (torch.arange(D, device=DEV) % 16 == 3)  # a few channels of K are larger, as in trained models
     kc, ks = _quantise(k, code)
     del k
-    vc, vs = _quantise(_normal(g, n_pages, H_kv, D, PAGE), code)
+    vc, vs = _quantise(_normal(g, n_pages, H_kv, PAGE, D), code)
     return dict(k_codes=kc, v_codes=vc, k_scale=ks, v_scale=vs)
 
 
@@ -366,11 +366,10 @@ def _append(st):
     t = slot - start
     fresh, old = (t >= 0) & (t < count), t < 0
     t = t.clamp(0, n_new - 1)
-    for name, x, flip in (("k", st["k"], False), ("v", st["v"], True)):
+    for name, x in (("k", st["k"]), ("v", st["v"])):
         codes, scales = st[name + "_codes"], st[name + "_scale"]
         new = x[b[:, None], t].float().transpose(1, 2)                # [touched, H_kv, 64, D]
         was = _raw(codes)[page].view(codes.dtype).float()
-        was = was.transpose(2, 3) if flip else was
         f4, o4 = fresh[:, None, :, None], old[:, None, :, None]
         amax = torch.where(f4 & torch.isfinite(new), new, torch.zeros_like(new)).abs().amax((-1, -2))
         s_old = torch.where(old.any(1)[:, None], scales[page], torch.zeros_like(amax))
@@ -378,9 +377,7 @@ def _append(st):
         inv = torch.where(s > 0, 1.0 / torch.where(s > 0, s, torch.ones_like(s)), torch.zeros_like(s))[..., None, None]
         got = _code(torch.where(f4, new * inv, was * (s_old[..., None, None] * inv)), code)
         keep = f4 | o4
-        raw = torch.where(keep, _raw(got), _raw(_code(was, code)))
-        raw = raw.transpose(2, 3) if flip else raw
-        _raw(codes)[page] = raw.contiguous()
+        _raw(codes)[page] = torch.where(keep, _raw(got), _raw(_code(was, code)))
         scales[page] = s
     h = torch.arange(H_kv, device=DEV)[None, :, None]
     bb, ss = b[:, None, None], slot[:, None, :]
@@ -391,12 +388,10 @@ def _append(st):
     return _cache_outputs(st)
 
 
-def _values(d, flip, dtype=torch.float32):
+def _values(d, name, dtype=torch.float32):
     """The cache's values in slot order, [B, H_kv, slots, D]."""
-    codes, scale = (d["v_codes"], d["v_scale"]) if flip else (d["k_codes"], d["k_scale"])
-    table = d["table"].long()
-    x = _raw(codes)[table].view(codes.dtype).to(dtype)                 # [B, pages, H_kv, 64, D] or [.., D, 64]
-    x = x.transpose(3, 4) if flip else x
+    codes, scale, table = d[name + "_codes"], d[name + "_scale"], d["table"].long()
+    x = _raw(codes)[table].view(codes.dtype).to(dtype)                 # [B, pages, H_kv, 64, D]
     x = x * scale.to(dtype)[table][..., None, None]
     B, P, H_kv, _, D = x.shape
     return x.transpose(1, 2).reshape(B, H_kv, P * PAGE, D)
@@ -427,7 +422,7 @@ def _unmasked(st, S):
 def _attend(st):
     case = st["case"]
     B, H, H_kv, n_q, D = case["B"], case["H"], case["H_kv"], case["n_q"], case["D"]
-    k = _values(st, False)
+    k = _values(st, "k")
     S = k.shape[2]
     q = st["q"].float().view(B, n_q, H_kv, H // H_kv, D).permute(0, 2, 3, 1, 4)   # [B, H_kv, G, n_q, D]
     s = torch.matmul(q.reshape(B, H_kv, -1, D), k.transpose(2, 3)).view(B, H_kv, H // H_kv, n_q, S) * st["scale"]
@@ -438,7 +433,7 @@ def _attend(st):
     total = p.sum(-1, keepdim=True)
     p = p / torch.where(total > 0, total, torch.ones_like(total))
     lse = (m + torch.log(total))[..., 0].reshape(B, H, n_q)
-    o = torch.matmul(p.view(B, H_kv, -1, S), _values(st, True)).view(B, H_kv, H // H_kv, n_q, D)
+    o = torch.matmul(p.view(B, H_kv, -1, S), _values(st, "v")).view(B, H_kv, H // H_kv, n_q, D)
     if case["accumulate"]:
         st["weight"] += p.sum((2, 3))
     return [o.permute(0, 3, 1, 2, 4).reshape(B, n_q, H, D).to(torch.bfloat16), lse, st["weight"]]
@@ -485,15 +480,13 @@ def _evict(st):
     page = st["table"].long().gather(1, (at // PAGE).view(B, -1)).view(B, H_kv, -1)
     block_used = (torch.arange(pages, device=DEV) * PAGE < new_len[:, None])      # [B, pages]
     to = dst["table"].long()
-    for name, flip in (("k", False), ("v", True)):
-        raw = _raw(st[name + "_codes"])
-        x = (raw[page, h, :, at % PAGE] if flip else raw[page, h, at % PAGE]).view(st[name + "_codes"].dtype).float()
+    for name in ("k", "v"):
+        x = _raw(st[name + "_codes"])[page, h, at % PAGE].view(st[name + "_codes"].dtype).float()
         x = x * st[name + "_scale"][page, h][..., None]
         x = torch.where(live[..., None], x, torch.zeros_like(x)).view(B, H_kv, pages, PAGE, D).transpose(1, 2)
         codes, s = _quantise(x, case["code"])                                     # [B, pages, H_kv, 64, D]
-        new = _raw(codes.transpose(3, 4).contiguous() if flip else codes)
         out = _raw(dst[name + "_codes"])
-        out[to] = torch.where(block_used[:, :, None, None, None], new, out[to])
+        out[to] = torch.where(block_used[:, :, None, None, None], _raw(codes), out[to])
         dst[name + "_scale"][to] = torch.where(block_used[:, :, None], s, dst[name + "_scale"][to])
     dst["weight"].copy_(torch.where(live, w.gather(-1, at), dst["weight"]))
     dst["pos"].copy_(torch.where(live, st["pos"].gather(-1, at), dst["pos"]))
@@ -555,7 +548,7 @@ def _exact_attend(case, st):
             k = (_raw(st["k_codes"])[pages, hk].view(st["k_codes"].dtype).double()
                  * st["k_scale"].double()[pages, hk, None, None]).reshape(-1, D)[:n]
             v = (_raw(st["v_codes"])[pages, hk].view(st["v_codes"].dtype).double()
-                 * st["v_scale"].double()[pages, hk, None, None]).transpose(1, 2).reshape(-1, D)[:n]
+                 * st["v_scale"].double()[pages, hk, None, None]).reshape(-1, D)[:n]
             j = torch.arange(n, device=DEV) if st["pos"] is None else st["pos"][b, hk, :n].long()
             q = st["q"][b, :, hk * G:(hk + 1) * G].double()                      # [n_q, G, D]
             s = st["scale"] * torch.einsum("tgd,nd->tgn", q, k)
@@ -602,9 +595,8 @@ def _exact_evict(case, st):
     weight = dst["weight"].double().cpu().numpy()
     scales = [dst[n + "_scale"].double().cpu().numpy() for n in ("k", "v")]
     # the largest magnitude of each slot, [page, H_kv, 64]
-    big = [_raw(st["k_codes"]).view(st["k_codes"].dtype).float().abs().amax(3).double(),
-           _raw(st["v_codes"]).view(st["v_codes"].dtype).float().abs().amax(2).double()]
-    big = [(x * st[n + "_scale"].double()[:, :, None]).cpu().numpy() for x, n in zip(big, ("k", "v"))]
+    big = [(st[n + "_codes"].float().abs().amax(3).double() * st[n + "_scale"].double()[:, :, None]).cpu().numpy()
+           for n in ("k", "v")]
     w = st["weight"].double().cpu().numpy()
     for b in range(B):
         n = int(st["len"][b])
