@@ -288,6 +288,137 @@ fm_status fm_attn_bwd_noalloc(const fm_attn_args* a, const fm_mask_meta* meta, c
                               const void* o, const float* lse, const void* dout, void* dq, void* dk, void* dv,
                               fm_stream_t stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Serving: a paged K/V cache held in 8 bits, its attention, and its eviction.  (No counterpart
+ * in the paper; the mask vectors, row numbering, head groups and conventions are those above.)
+ * ------------------------------------------------------------------------------------------ */
+
+/* Slots of a cache page; a page of one K/V head is also the block that shares one scale. */
+#define FM_CACHE_PAGE 64
+
+/*
+ * A K/V cache of one layer: device pointers into the caller's buffers.
+ *   Slot s of sequence b lies in page page_table[b, s / 64], at s % 64 in it.  A key's value is
+ *   its code times the scale of its (page, head):
+ *     k_codes, v_codes  [n_pages, H_kv, 64, D], 16-byte aligned; code_type 0: int8 in
+ *                       [-127, 127], 1: 8-bit floats e4m3 (no NaN code is ever written)
+ *     k_scale, v_scale  fp32 [n_pages, H_kv]
+ *     page_table        int32 [B, max_pages].  An entry outside [0, n_pages) is a page that is not
+ *                       there: its slots are written by no call and read as masked.
+ *     weight            fp32 [B, H_kv, max_pages * 64] or NULL: attention weight that each slot's
+ *                       key has received so far
+ *     pos               int32 [B, H_kv, max_pages * 64] or NULL: row index (position in the
+ *                       sequence) of each slot's token; NULL: the slot index itself.  Each head has
+ *                       its own, since an eviction keeps other tokens in each head.
+ *   Scale rule: with amax the largest finite |x| of the block and Qmax 127 (int8) or 448 (e4m3), the
+ *   scale is 0 if amax = 0, else the smallest power of two 2^e >= amax / Qmax, e >= -126; codes are
+ *   x / scale rounded to nearest, ties to even, after clamping to [-Qmax, Qmax] (so infinities
+ *   saturate); NaN becomes 0.  Powers of two make the division exact, so a code has one rounding.
+ *   D is 64, 128 or 256; n_pages * H_kv * 64 and B * H_kv * max_pages * 64 are below 2^31; B <= 2048.
+ */
+typedef struct {
+  int32_t B, H_kv, D, n_pages, max_pages;
+  int32_t code_type; /* 0 = int8, 1 = e4m3 */
+  void* k_codes;
+  void* v_codes;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* page_table;
+  float* weight;
+  int32_t* pos;
+} fm_kv_cache;
+
+/*
+ * Writes new tokens into a cache: token t < count[b] of sequence b goes to slot start[b] + t.
+ * A block that gets tokens behind older ones takes the larger of its scale and the new tokens'
+ * scale by the rule above; where it grows, the older codes are re-quantised (code * old / new,
+ * rounded to nearest even).  weight (if present) of each new slot becomes 0 and pos (if present)
+ * row[b] + t.  Slots behind the last new token keep what they held.  Tokens whose slot is negative,
+ * past the table or in a page that is not there are left out.
+ *   k, v    device [B, n_new, H_kv, D], 16-byte aligned, of `dtype` (0 = bf16, 1 = fp32)
+ *   start   device int32 [B]: tokens in the cache before the call
+ *   count   device int32 [B] or NULL (n_new each); values are clamped to [0, n_new]
+ *   row     device int32 [B] or NULL (= start): row index of the first new token
+ *   No page may appear twice among the blocks that get tokens.
+ * Errors: FM_ERR_INVALID_ARG, FM_ERR_UNSUPPORTED, FM_ERR_CUDA.
+ */
+fm_status fm_cache_append(const fm_kv_cache* cache, const void* k, const void* v, int32_t dtype, int32_t n_new,
+                          const int32_t* start, const int32_t* count, const int32_t* row, fm_stream_t stream);
+
+/* Attention of a few query rows per sequence over a cache. */
+typedef struct {
+  int32_t H, n_q;     /* H_kv divides H, at most 64 query heads per K/V head; n_q * H / H_kv <= 1024 */
+  int32_t dtype;      /* of q and o: 0 = bf16 */
+  float scale;        /* softmax scale, > 0 and finite */
+  const void* q;      /* device [B, n_q, H, D], 16-byte aligned */
+  const int32_t* len; /* device int32 [B]: slots in use (clamped to [0, max_pages * 64]) */
+  const int32_t* row; /* device int32 [B]: row index of each sequence's first query (query t is row
+                         row[b] + t); may be NULL if there are no vectors and causal = 0 */
+  const int32_t* vec[4]; /* mask vectors LTS, LTE, UTS, UTE, device int32 [B, Hm, n_k], read at each key's pos;
+                            NULL: LTS, LTE = 2^31 - 1 (no last row is known here), UTS, UTE = 0.  Keys whose
+                            pos lies outside [0, n_k) are masked by no vector. */
+  int32_t Hm, n_k;    /* Hm = 1 or H; both 0 without vectors */
+  int32_t causal;     /* 1: a key is also masked for the rows before its pos */
+  int32_t accumulate; /* 1: add the weight each key receives to cache->weight */
+} fm_cache_attn_args;
+
+/* Bytes of workspace fm_cache_attn needs (0 if the arguments are invalid; device pointers are not read). */
+size_t fm_cache_attn_workspace_bytes(const fm_kv_cache* cache, const fm_cache_attn_args* a);
+
+/*
+ * For every sequence b, query t and head h, with U the unmasked keys among the first len[b] slots of
+ * K/V head h / (H / H_kv):  O = sum_{j in U} softmax_j(scale q.k_j) v_j and
+ * LSE = ln sum_{j in U} exp(scale q.k_j); U empty: O = 0, LSE = -inf (as fm_attn_fwd).  Blocks whose
+ * keys are masked for every row are not read.  accumulate = 1: weight[b, hk, j] += the sum of key j's
+ * softmax weights over the rows of the heads that share hk.  Every sum has a fixed order: the same
+ * call gives the same bits.
+ *   o    device [B, n_q, H, D] of the dtype, lse device fp32 [B, H, n_q]
+ *   ws   device workspace, ws_bytes >= fm_cache_attn_workspace_bytes(cache, a), 256-byte aligned.
+ *        Holds nothing between calls; calls that may overlap on the GPU need one each.
+ * Errors: FM_ERR_INVALID_ARG, FM_ERR_UNSUPPORTED, FM_ERR_WORKSPACE, FM_ERR_CUDA.
+ */
+fm_status fm_cache_attn(const fm_kv_cache* cache, const fm_cache_attn_args* a, void* o, float* lse, void* ws,
+                        size_t ws_bytes, fm_stream_t stream);
+
+/*
+ * Attention weight that each key of a prompt receives (what fm_cache_attn accumulates, for the rows
+ * of fm_attn_fwd):  weight[b, hk, j] (+)= sum over the query heads h that share hk and the rows i that
+ * see key j of exp(scale q_i.k_j - LSE_i).  Rows with LSE = -inf see no key.
+ *   a       as for fm_attn_fwd, dtype 0 only; a->v is not read and may be NULL.
+ *   meta, vec  as for fm_attn_fwd.
+ *   lse     fp32 [B, H, n_q], fm_attn_fwd's
+ *   weight  fp32, row (b, hk) at weight + (b * H_kv + hk) * weight_stride, n_k values each
+ *           (weight_stride >= n_k; a cache's weight takes max_pages * 64)
+ *   accumulate  0: overwrite, 1: add
+ * The sums have a fixed order: the same call gives the same bits.
+ * Errors: FM_ERR_INVALID_ARG, FM_ERR_UNSUPPORTED, FM_ERR_CUDA.
+ */
+fm_status fm_attn_key_weight(const fm_attn_args* a, const fm_mask_meta* meta, const int32_t* const vec[4],
+                             const float* lse, float* weight, int64_t weight_stride, int32_t accumulate,
+                             fm_stream_t stream);
+
+/* Bytes of workspace fm_cache_evict needs (0 if the arguments are invalid). */
+size_t fm_cache_evict_workspace_bytes(const fm_kv_cache* src, int32_t budget);
+
+/*
+ * Evicts the keys that received the least attention: for every sequence b and K/V head, of the len[b]
+ * slots in use the last `recent` are kept, and of the others those budget - recent with the largest
+ * src->weight (ties: the lowest slot; NaN counts as the largest).  A sequence with len[b] <= budget
+ * keeps all its slots.  What is kept goes, in slot order, to slots 0, 1, ... of dst with its weight and
+ * pos, each dst block re-quantised by the scale rule over the values it now holds; slots behind the
+ * last one in its block get code 0, whole blocks behind it and their weight and pos are not written.
+ * new_len[b] = min(len[b], budget).
+ *   src, dst  same B, H_kv, D, code_type; src->weight is needed; dst may lie in the same pools
+ *             as src, with a table of other pages: a page of dst must not be a page of src that is in
+ *             use.  dst->weight and dst->pos may be NULL; src->pos NULL = the slot index.
+ *   len       device int32 [B]; new_len device int32 [B] (may be len itself)
+ *   budget    1 <= budget <= 64 * dst->max_pages; 0 <= recent <= budget
+ *   ws        device workspace, 256-byte aligned; calls that may overlap on the GPU need one each
+ * Errors: FM_ERR_INVALID_ARG, FM_ERR_UNSUPPORTED, FM_ERR_WORKSPACE, FM_ERR_CUDA.
+ */
+fm_status fm_cache_evict(const fm_kv_cache* src, const fm_kv_cache* dst, const int32_t* len, int32_t budget,
+                         int32_t recent, int32_t* new_len, void* ws, size_t ws_bytes, fm_stream_t stream);
+
 /*
  * Reads and clears the current device's status word: FM_OK, or
  * FM_ERR_DEVICE_TIMEOUT if a kernel gave up on a bounded wait since the last

@@ -13,6 +13,12 @@ Entry points (same names as the C ABI):
   fm_varlen_mask(cu_seqlens, N, causal)             -> 4 tensors [1, 1, N]
   fm_attn_fwd(q, k, v, meta, vecs, scale)           -> (o, lse)
   fm_attn_bwd(q, k, v, o, lse, do, meta, vecs, scale, deterministic=False) -> (dq, dk, dv)
+Serving, over a paged 8-bit K/V cache (kvcache.py):
+  KVCache(...), fm_cache_alloc(...)                 the cache's tensors
+  fm_cache_append(cache, k, v, start)               quantises and writes new tokens
+  fm_cache_attn(cache, q, cache_len, scale)         -> (o, lse) of a few query rows per sequence
+  fm_attn_key_weight(q, k, lse, meta, vecs, scale)  -> attention weight per prompt key
+  fm_cache_evict(src, dst, cache_len, budget)       -> new lengths; keeps the heaviest keys
 """
 from __future__ import annotations
 
@@ -62,6 +68,20 @@ class AttnArgs(ctypes.Structure):
 VecArray = ctypes.c_void_p * 4
 
 
+class KVCacheC(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("H_kv", ctypes.c_int32), ("D", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("code_type", ctypes.c_int32), ("k_codes", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("pos", ctypes.c_void_p)]
+
+
+class CacheAttnArgs(ctypes.Structure):
+    _fields_ = [("H", ctypes.c_int32), ("n_q", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("q", ctypes.c_void_p), ("len", ctypes.c_void_p), ("row", ctypes.c_void_p), ("vec", VecArray),
+                ("Hm", ctypes.c_int32), ("n_k", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("accumulate", ctypes.c_int32)]
+
+
 def lib():
     """Load the CUDA library (raises if it has not been built)."""
     global _lib
@@ -89,6 +109,20 @@ def lib():
         L.fm_attn_bwd.argtypes = [ctypes.POINTER(AttnArgs), ctypes.POINTER(MaskMetaC), VecArray, vp, vp, vp, vp, vp,
                                   vp, vp, sz, vp]
         L.fm_attn_bwd.restype = ctypes.c_int
+        cache, cargs = ctypes.POINTER(KVCacheC), ctypes.POINTER(CacheAttnArgs)
+        L.fm_cache_append.argtypes = [cache, vp, vp, i32, i32, vp, vp, vp, vp]
+        L.fm_cache_append.restype = ctypes.c_int
+        L.fm_cache_attn_workspace_bytes.argtypes = [cache, cargs]
+        L.fm_cache_attn_workspace_bytes.restype = sz
+        L.fm_cache_attn.argtypes = [cache, cargs, vp, vp, vp, sz, vp]
+        L.fm_cache_attn.restype = ctypes.c_int
+        L.fm_attn_key_weight.argtypes = [ctypes.POINTER(AttnArgs), ctypes.POINTER(MaskMetaC), VecArray, vp, vp,
+                                         ctypes.c_int64, i32, vp]
+        L.fm_attn_key_weight.restype = ctypes.c_int
+        L.fm_cache_evict_workspace_bytes.argtypes = [cache, i32]
+        L.fm_cache_evict_workspace_bytes.restype = sz
+        L.fm_cache_evict.argtypes = [cache, cache, vp, i32, i32, vp, vp, sz, vp]
+        L.fm_cache_evict.restype = ctypes.c_int
         L.fm_get_device_status.argtypes = [vp]
         L.fm_get_device_status.restype = ctypes.c_int
         L.fm_selftest_wait_timeout.argtypes = [vp]
@@ -338,3 +372,7 @@ def fm_selftest_wait_timeout(stream=None):
 
 def fm_get_device_status(stream=None) -> int:
     return int(lib().fm_get_device_status(_stream(stream)))
+
+
+from .kvcache import (CACHE_PAGE, KVCache, fm_attn_key_weight, fm_cache_alloc, fm_cache_append,  # noqa: E402,F401
+                      fm_cache_attn, fm_cache_attn_workspace_bytes, fm_cache_evict, fm_cache_evict_workspace_bytes)

@@ -75,6 +75,21 @@ bool encode_tmap_f32_4d(CUtensorMap* map, const void* base, uint64_t D, uint64_t
   return r == CUDA_SUCCESS;
 }
 
+// 2-D map over rows of row_bytes bytes (64, or a multiple of 128): box (min(row_bytes, 128), box_rows), swizzled
+// over the box row's span (64 or 128 bytes).
+bool encode_tmap_u8_rows(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_rows) {
+  EncodeTiledFn enc = get_encode();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {row_bytes, rows};
+  cuuint64_t strides[1] = {row_bytes};
+  cuuint32_t box[2] = {row_bytes < 128 ? (cuuint32_t)row_bytes : 128u, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, row_bytes < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // One CTA waits on an mbarrier that nothing arrives on.  The bounded wait gives
 // up after kTimeoutNs and records FM_ERR_DEVICE_TIMEOUT (site 0x7E57) in the
 // device status word; the kernel then returns normally.

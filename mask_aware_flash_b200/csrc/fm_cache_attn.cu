@@ -1,0 +1,996 @@
+// Attention of a few query rows per sequence over the paged 8-bit K/V cache (fm_cache_attn).
+//
+// The path is bound by the bytes of the cache: every live key's K and V codes are read once, 2 D bytes
+// per key and K/V head, and each is used for the n_q * H / H_kv rows that share the head.  So the design
+// starts from the copies:
+//   * the (sequence, K/V head, 64-token block) units of the whole batch form one flat order that is cut
+//     into equal runs, one per CTA (one CTA per SM): ragged lengths and long single sequences load every
+//     SM alike.  A (sequence, head) cut by a run's border is joined by the second kernel.
+//   * each warp owns a ring of K and V blocks in shared memory, filled by TMA (64 rows of D codes, 64- or
+//     128-byte swizzle) through mbarriers, and works through its share of the run's blocks alone: no CTA
+//     barrier until a (sequence, head) ends.
+//   * blocks that no row sees are found from the mask vectors before anything of them is loaded.
+// The products run on mma.sync m16n8k16 with fp16 operands and fp32 accumulation, as
+//   S^T [keys x rows] = K Q^T   and   O^T [d x rows] += V^T P^T,
+// so that the 8 columns of the instruction are the few query rows and no row of it is padding for up to
+// 8 rows.  (tcgen05 wants its operands as 16-bit tiles in shared memory or TMEM: converting the codes
+// there and back would move three times the bytes per block that this form does, for a path that needs
+// under a third of mma.sync's rate.)  Both 8-bit formats are exact in fp16, so a score is the exact
+// product of q and the cached key, summed in fp32.  The contraction orders are permuted so that a thread's
+// operands are 16 consecutive bytes of a row: over d for K; for V by pairing the bytes of two tokens.
+#include "fm_cache.cuh"
+
+namespace fm {
+namespace {
+
+constexpr int kSMs = 148;
+constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// P is held as 2^14 p in fp16: p down to 2^-28 keeps all 11 bits (half a unit is 2^-12 of p), and 2^14 is
+// exact, so a row that sees one key returns its value unrounded.
+constexpr float kPBias = 14.f;
+
+struct CacheAttnParams {
+  const __nv_bfloat16* q;
+  const int32_t* len;
+  const int32_t* row;
+  const int32_t* vec[4];
+  const int32_t* page_table;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* pos;
+  float* weight;
+  __nv_bfloat16* o;
+  float* lse;
+  // workspace
+  int32_t* units;    // [B + 1] units before each sequence
+  float* part_o;     // [n_work][2][n_rows_pad][D] partial sums of runs that end inside a (sequence, head)
+  float2* part_ml;   // [n_work][2][n_rows_pad] their running maximum (log2) and sum
+  float2* whole_ml;  // [B * H_kv][n_rows_pad] the same for (sequence, head)s inside one run (accumulate)
+  float* score;      // [B * H_kv][max_pages * 64][rows4] scores in log2 units (accumulate)
+  uint8_t* live;     // [B * H_kv][max_pages] block was read (accumulate)
+  int* status;
+  int B, H, H_kv, n_q, group, n_rows, n_rows_pad, rows4, Hm, n_k, n_pages, max_pages, n_work, n_chunks;
+  int masked, causal, accumulate;
+  float scale_log2;
+};
+
+template <int D, int NT>
+struct CacheAttnCfg {
+  static constexpr int kWarps = D == 256 ? 4 : 8;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kSlots = D == 64 ? 4 : 2;     // ring slots of a warp (each one K or one V block)
+  static constexpr int kBox = D < 128 ? D : 128;     // bytes of a TMA box row (= swizzle span)
+  static constexpr int kBoxes = D / kBox;
+  static constexpr int kSlotBytes = kPage * D;
+  static constexpr int kRows = 8 * NT;               // query rows a CTA holds
+  static constexpr int kKSteps = D / 16;
+  static constexpr int kCap = 512;                   // units listed at a time
+  static constexpr int kRing = 0;
+  static constexpr int kQ = kRing + kWarps * kSlots * kSlotBytes;       // fragments [NT][D / 16][32] x 8 bytes
+  static constexpr int kTree = kQ + NT * kKSteps * 32 * 8;              // [warps / 2][regs][32] fp32
+  static constexpr int kRegs = D / 16 * NT * 4;
+  static constexpr int kList = kTree + kWarps / 2 * kRegs * 32 * 4;     // int4 entries
+  static constexpr int kSegStart = kList + kCap * 16;                   // int [kCap + 1] (padded)
+  static constexpr int kSegBh = kSegStart + (kCap + 4) * 4;             // int [kCap]
+  static constexpr int kSegFlag = kSegBh + kCap * 4;                    // int [kCap]: 1 begins, 2 ends here
+  static constexpr int kCls = kSegFlag + kCap * 4;                      // uint8 [kCap]
+  static constexpr int kMl = kCls + kCap;                               // float2 [warps][rows]
+  static constexpr int kQs = kMl + kWarps * kRows * 8;                  // float [rows]
+  static constexpr int kBits = kQs + kRows * 4;                         // uint2 [warps][rows] mask bits
+  static constexpr int kBar = kBits + kWarps * kRows * 8;               // mbarriers [warps][slots]
+  static constexpr int kMisc = kBar + kWarps * kSlots * 8;              // abort, zero, scan totals
+  static constexpr int kRed = kMisc + 32;                               // uint32 [32]
+  static constexpr int kUnits = kRed + 128;                             // int [B + 1] (dynamic)
+};
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::
+          "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+// D (fp32, 16 x 8) += A (fp16, 16 x 16) B (fp16, 16 x 8)
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// transpose of the 8 x 8 matrix of 16-bit elements that the warp holds one pair per lane
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Bounds of one cached key: its row index and its two masked stretches.
+struct KeyBounds {
+  int j, lts, lte, uts, ute;
+  bool in;  // slot in use
+};
+__device__ __forceinline__ void load_pos(const CacheAttnParams& p, KeyBounds& k, int64_t bh, int slot, int len) {
+  k.in = slot < len;
+  k.j = slot;
+  if (k.in && p.pos) k.j = __ldg(p.pos + bh * p.max_pages * kPage + slot);
+}
+__device__ __forceinline__ void load_vectors(const CacheAttnParams& p, KeyBounds& k, int64_t bhm) {
+  k.lts = k.lte = 0x7FFFFFFF;  // canonical empty stretches; also those of keys outside the vectors
+  k.uts = k.ute = 0;
+  if (k.in && k.j >= 0 && k.j < p.n_k) {
+    const int64_t at = bhm * p.n_k + k.j;
+    if (p.vec[0]) k.lts = __ldg(p.vec[0] + at);
+    if (p.vec[1]) k.lte = __ldg(p.vec[1] + at);
+    if (p.vec[2]) k.uts = __ldg(p.vec[2] + at);
+    if (p.vec[3]) k.ute = __ldg(p.vec[3] + at);
+  }
+}
+__device__ __forceinline__ bool key_seen(const CacheAttnParams& p, const KeyBounds& k, int i) {
+  return k.in && !(p.causal && k.j > i) && !(k.lts <= i && i < k.lte) && !(k.uts <= i && i < k.ute);
+}
+
+// Sequence of a unit: the largest b with units[b] <= u.
+__device__ __forceinline__ int find_seq(const int* units, int B, int u) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (units[mid] <= u) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+template <int D, int NT, bool E4M3>
+__global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
+    cache_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const CacheAttnParams p) {
+  using C = CacheAttnCfg<D, NT>;
+  constexpr int kWarps = C::kWarps, kThreads = C::kThreads, kSlots = C::kSlots;
+  constexpr int kTiles = D / 16;  // 16-row tiles of O^T
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_base_1024(smem_raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int work = blockIdx.x / p.n_chunks, chunk = blockIdx.x % p.n_chunks;
+  const int row_base = chunk * C::kRows;  // first query row of this CTA
+
+  uint2* q_s = reinterpret_cast<uint2*>(smem + C::kQ);
+  float* tree = reinterpret_cast<float*>(smem + C::kTree);
+  int4* list = reinterpret_cast<int4*>(smem + C::kList);
+  int* seg_start = reinterpret_cast<int*>(smem + C::kSegStart);
+  int* seg_bh = reinterpret_cast<int*>(smem + C::kSegBh);
+  int* seg_flag = reinterpret_cast<int*>(smem + C::kSegFlag);
+  uint8_t* cls = smem + C::kCls;
+  float2* ml_s = reinterpret_cast<float2*>(smem + C::kMl);
+  float* qs_s = reinterpret_cast<float*>(smem + C::kQs);
+  uint2* bits_s = reinterpret_cast<uint2*>(smem + C::kBits) + warp * C::kRows;
+  int* misc = reinterpret_cast<int*>(smem + C::kMisc);
+  volatile int* abort_flag = misc;
+  const volatile int* never = misc + 1;
+  uint32_t* red = reinterpret_cast<uint32_t*>(smem + C::kRed);
+  int* units = reinterpret_cast<int*>(smem + C::kUnits);
+  const uint32_t ring = smem_u32(smem + C::kRing) + warp * kSlots * C::kSlotBytes;
+  const uint8_t* ring_p = smem + C::kRing + warp * kSlots * C::kSlotBytes;
+  const uint32_t bar0 = smem_u32(smem + C::kBar) + warp * kSlots * 8;
+
+  if (threadIdx.x == 0) {
+    misc[0] = misc[1] = 0;
+    for (int i = 0; i < kWarps * kSlots; ++i) mbar_init(smem_u32(smem + C::kBar) + 8 * i, 1);
+    fence_barrier_init();
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  const int cap = p.max_pages * kPage;
+  for (int b = threadIdx.x; b < p.B; b += kThreads)
+    units[b + 1] = (min(max(__ldg(p.len + b), 0), cap) + kPage - 1) / kPage * p.H_kv;
+  __syncthreads();
+  if (warp == 0) {  // prefix sum over the sequences
+    int carry = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      int x = b0 + lane < p.B ? units[b0 + lane + 1] : 0;
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, s);
+        if (lane >= s) x += y;
+      }
+      if (b0 + lane < p.B) units[b0 + lane + 1] = carry + x;
+      carry += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) units[0] = 0;
+  }
+  __syncthreads();
+  const int total = units[p.B];
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b <= p.B; b += kThreads) p.units[b] = units[b];
+  const int per = (total + p.n_work - 1) / p.n_work;
+  const int c0 = min((int64_t)work * per, (int64_t)total), c1 = min(c0 + per, total);
+
+  float o[kTiles][NT][4];
+  float m[NT][2], l[NT][2];
+  float unit_v = 0.f, max_v = 0.f;  // O is held in units of unit_v (the V scale of the last block)
+  int item = 0;                     // ring items consumed by this warp so far
+  bool ok = true;
+
+  for (int w0 = c0; w0 < c1; w0 += C::kCap) {
+    const int nu = min(C::kCap, c1 - w0);
+    // -------------------------------------------------------- list the run's blocks (the live ones)
+    if (w0 != c0) __syncthreads();  // the last list has been read
+    if (p.masked) {
+      // one warp per block, two keys per lane: does any row see any key / every key?
+      for (int u = warp; u < nu; u += kWarps) {
+        const int b = find_seq(units, p.B, w0 + u);
+        const int len = min(max(__ldg(p.len + b), 0), cap), nb = (len + kPage - 1) / kPage;
+        const int rem = w0 + u - units[b], hk = rem / nb, blk = rem % nb;
+        const int64_t bh = (int64_t)b * p.H_kv + hk;
+        const int row0 = __ldg(p.row + b);
+        KeyBounds k[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) load_pos(p, k[i], bh, blk * kPage + lane + 32 * i, len);
+        bool any = false, all = true;
+        const int heads = p.Hm > 1 ? p.group : 1;
+        for (int hg = 0; hg < heads; ++hg) {
+          const int64_t bhm = p.Hm > 1 ? (int64_t)b * p.Hm + hk * p.group + hg : b;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) load_vectors(p, k[i], bhm);
+          for (int tq = 0; tq < p.n_q; ++tq) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const bool s = key_seen(p, k[i], row0 + tq);
+              any |= s;
+              all &= s;
+            }
+          }
+        }
+        any = __any_sync(0xffffffffu, any);
+        all = __all_sync(0xffffffffu, all);
+        if (lane == 0) cls[u] = any ? (all ? 2 : 1) : 0;
+      }
+      __syncthreads();
+    }
+    uint32_t mine = 0;  // live blocks | segment starts << 16 of this thread's units
+    constexpr int kPer = C::kCap / kThreads;
+    int4 ent[kPer];
+    int ubh[kPer], uflag[kPer];  // flags: 1 live, 2 first of its segment here, 4 last here, 8 begins, 16 ends
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int u = threadIdx.x * kPer + i;
+      uflag[i] = 0;
+      if (u >= nu) continue;
+      const int b = find_seq(units, p.B, w0 + u);
+      const int len = min(max(__ldg(p.len + b), 0), cap), nb = (len + kPage - 1) / kPage;
+      const int rem = w0 + u - units[b], hk = rem / nb, blk = rem % nb;
+      const int page = __ldg(p.page_table + (int64_t)b * p.max_pages + blk);
+      const bool there = page >= 0 && page < p.n_pages;
+      const int c = !there ? 0 : p.masked ? cls[u] : ((blk + 1) * kPage > len ? 1 : 2);
+      ubh[i] = b * p.H_kv + hk;
+      if (c) {
+        const int at = page * p.H_kv + hk;
+        ent[i] = make_int4(at * kPage, blk * kPage + (c == 1 ? 1 : 0), __float_as_int(__ldg(p.k_scale + at)),
+                           __float_as_int(__ldg(p.v_scale + at)));
+        uflag[i] |= 1;
+      }
+      if (p.accumulate && chunk == 0) p.live[(int64_t)ubh[i] * p.max_pages + blk] = c != 0;
+      if (u == 0 || blk == 0) uflag[i] |= 2;
+      if (u == nu - 1 || blk == nb - 1) uflag[i] |= 4;
+      if (w0 + u == c0 || blk == 0) uflag[i] |= 8;
+      if (w0 + u == c1 - 1 || blk == nb - 1) uflag[i] |= 16;
+      mine += (uflag[i] & 1) + ((uflag[i] & 2) << 15);
+    }
+    uint32_t incl = mine;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, s);
+      if (lane >= s) incl += y;
+    }
+    if (lane == 31) red[warp] = incl;
+    __syncthreads();
+    uint32_t before = incl - mine, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += red[w];
+      all += red[w];
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (uflag[i] & 2) {
+        const int k = before >> 16;
+        seg_start[k] = before & 0xFFFFu;
+        seg_bh[k] = ubh[i];
+        seg_flag[k] = (uflag[i] & 8) ? 1 : 0;
+      }
+      before += (uflag[i] & 1) + ((uflag[i] & 2) << 15);
+      if (uflag[i] & 1) list[(before & 0xFFFFu) - 1] = ent[i];
+    }
+    __syncthreads();
+    // "ends here" goes on top once every segment's word is there (segment starts before a unit, its own included)
+    {
+      uint32_t run = incl - mine;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w)
+        if (w < warp) run += red[w];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        run += (uflag[i] & 1) + ((uflag[i] & 2) << 15);
+        if ((uflag[i] & 4) && (uflag[i] & 16)) seg_flag[(run >> 16) - 1] |= 2;
+      }
+    }
+    const int n_live = all & 0xFFFFu, n_seg = all >> 16;
+    if (threadIdx.x == 0) seg_start[n_seg] = n_live;
+    __syncthreads();
+
+    // ---------------------------------------------------------------- the ring of this warp
+    const int n_items = 2 * (n_live > warp ? (n_live - warp + kWarps - 1) / kWarps : 0);
+    int issued = 0, done = 0;
+    auto issue = [&]() {  // the next item: K of a block, then its V
+      if (issued < n_items && ok) {
+        if (lane == 0) {
+          const int4 e = list[warp + kWarps * (issued >> 1)];
+          const int slot = (item + issued) % kSlots;
+          const uint32_t bar = bar0 + 8 * slot;
+          mbar_arrive_expect_tx(bar, C::kSlotBytes);
+#pragma unroll
+          for (int x = 0; x < C::kBoxes; ++x)
+            tma_load_2d(ring + slot * C::kSlotBytes + x * kPage * C::kBox, (issued & 1) ? &tm_v : &tm_k, bar, x * C::kBox,
+                        e.x);
+        }
+        ++issued;
+      }
+    };
+    auto wait = [&]() {  // the item to be consumed next has arrived
+      const int it = item + done;
+      if (ok && !__all_sync(0xffffffffu, mbar_wait(bar0 + 8 * (it % kSlots), (it / kSlots) & 1, abort_flag))) {
+        // gave up: the warp goes on to take part in the CTA's barriers, but issues nothing more; its copies in
+        // flight must land before the ring can be left
+        ok = false;
+        if (lane == 0) {
+          record_failure(p.status, abort_flag, 51);
+          for (int i = done; i < issued; ++i) mbar_wait(bar0 + 8 * ((item + i) % kSlots), ((item + i) / kSlots) & 1, never);
+        }
+      }
+    };
+    for (int i = 0; i < kSlots; ++i) issue();
+
+    // query rows of a segment into shared memory as fragments: row n of tile n / 8, scaled by a power of
+    // two that puts its largest element into [2^14, 2^15) (exact; bf16's range is wider than fp16's, and
+    // elements under 2^-28 of the largest lose low bits, at most 2^-39 of the row's largest)
+    constexpr int kQRows = C::kRows / kWarps > 0 ? C::kRows / kWarps : 1;
+    constexpr int kQElems = D / 32;  // consecutive elements per lane
+    uint32_t qreg[kQRows][kQElems / 2];
+    auto load_q = [&](int bh) {
+#pragma unroll
+      for (int i = 0; i < kQRows; ++i) {
+        const int n = warp + kWarps * i, r = row_base + n;
+#pragma unroll
+        for (int x = 0; x < kQElems / 2; ++x) qreg[i][x] = 0;
+        if (n < C::kRows && r < p.n_rows) {
+          const int b = bh / p.H_kv, hk = bh % p.H_kv;
+          const int h = hk * p.group + r / p.n_q, tq = r % p.n_q;
+          const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + (((int64_t)b * p.n_q + tq) * p.H + h) * D) +
+                                lane * (kQElems / 2);
+#pragma unroll
+          for (int x = 0; x < kQElems / 2; ++x) qreg[i][x] = __ldg(src + x);
+        }
+      }
+    };
+    auto store_q = [&]() {
+#pragma unroll
+      for (int i = 0; i < kQRows; ++i) {
+        const int n = warp + kWarps * i;
+        if (n >= C::kRows) continue;
+        float amax = 0.f;
+#pragma unroll
+        for (int x = 0; x < kQElems / 2; ++x) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(qreg[i][x])), fabsf(bf16_hi(qreg[i][x]))));
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
+        int e = 14 - ((int)(__float_as_uint(amax) >> 23) - 127);
+        e = amax > 0.f && amax <= 3.402823466e38f ? min(max(e, -126), 126) : 0;
+        const float f = __uint_as_float((uint32_t)(e + 127) << 23), back = __uint_as_float((uint32_t)(127 - e) << 23);
+        if (lane == 0) qs_s[n] = p.scale_log2 * back;
+        uint32_t h[kQElems / 2];
+#pragma unroll
+        for (int x = 0; x < kQElems / 2; ++x) h[x] = pack_f16(bf16_lo(qreg[i][x]) * f, bf16_hi(qreg[i][x]) * f);
+        // element d: 16-byte piece c = d / 16 of its box row; word s of the piece is k-step (.., s)
+#pragma unroll
+        for (int x = 0; x < kQElems / 2; ++x) {
+          const int d = lane * kQElems + 2 * x, in_box = d % C::kBox, c = in_box >> 4, s = (d & 15) >> 2;
+          const int tt = C::kBox == 128 ? c >> 1 : c, hh = C::kBox == 128 ? c & 1 : 0;
+          const int ks = d / C::kBox * (C::kBox / 16) + hh * 4 + s;
+          uint32_t* dst = reinterpret_cast<uint32_t*>(q_s + ((n >> 3) * C::kKSteps + ks) * 32 + (n & 7) * 4 + tt);
+          dst[(d >> 1) & 1] = h[x];
+        }
+      }
+    };
+    load_q(seg_bh[0]);
+    store_q();
+    __syncthreads();
+
+    for (int sg = 0; sg < n_seg; ++sg) {
+      const int bh = seg_bh[sg], flag = seg_flag[sg], e1 = seg_start[sg + 1];
+      const int b = bh / p.H_kv, hk = bh % p.H_kv;
+      const int len = min(max(__ldg(p.len + b), 0), cap);
+      if (sg + 1 < n_seg) load_q(seg_bh[sg + 1]);  // in flight during this segment
+      if (flag & 1) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          m[nt][0] = m[nt][1] = kNegInf;
+          l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[i][nt][c] = 0.f;
+        }
+        unit_v = max_v = 0.f;
+      }
+      for (int e = warp + kWarps * (done >> 1); e < e1; e += kWarps) {
+        const int4 ent = list[e];
+        const int slot0 = ent.y & ~1;
+        const bool partial = ent.y & 1;
+        const float ks = __int_as_float(ent.z), vs = __int_as_float(ent.w);
+        if (partial) {
+          // bit k of row n's word pair: the row sees key k of the block
+          KeyBounds k[2];
+          if (p.masked) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) load_pos(p, k[i], bh, slot0 + lane + 32 * i, len);
+            const int row0 = __ldg(p.row + b);
+            int at_head = -1;
+            for (int n = 0; n < C::kRows; ++n) {
+              const int r = min(row_base + n, p.n_rows - 1), hg = p.Hm > 1 ? r / p.n_q : 0;
+              if (hg != at_head) {
+                at_head = hg;
+                const int64_t bhm = p.Hm > 1 ? (int64_t)b * p.Hm + hk * p.group + hg : b;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) load_vectors(p, k[i], bhm);
+              }
+              const int i = row0 + r % p.n_q;
+              const uint32_t lo = __ballot_sync(0xffffffffu, key_seen(p, k[0], i));
+              const uint32_t hi = __ballot_sync(0xffffffffu, key_seen(p, k[1], i));
+              if (lane == (n & 31)) bits_s[n] = make_uint2(lo, hi);
+            }
+          } else {
+            const uint32_t lo = __ballot_sync(0xffffffffu, slot0 + lane < len);
+            const uint32_t hi = __ballot_sync(0xffffffffu, slot0 + lane + 32 < len);
+            if (lane < C::kRows) bits_s[lane] = make_uint2(lo, hi);
+          }
+          __syncwarp();
+        }
+        // ------------------------------------------------------------ S^T = K Q^T (64 keys x rows)
+        wait();
+        float s[4][NT][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s[j][nt][c] = 0.f;
+        {
+          const uint8_t* kb = ring_p + (item + done) % kSlots * C::kSlotBytes;
+#pragma unroll
+          for (int x = 0; x < C::kBoxes; ++x)
+#pragma unroll
+            for (int h = 0; h < (C::kBox == 128 ? 2 : 1); ++h) {
+              // key 16 j + 8 r + g, 16-byte piece 2 t + h (t for D = 64): no two lanes of a quarter warp
+              // share a bank under the swizzle
+              uint4 raw[4][2];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                  const int key = 16 * j + 8 * r + g;
+                  const int c = C::kBox == 128 ? ((2 * t + h) ^ (key & 7)) : (t ^ ((key >> 1) & 3));
+                  raw[j][r] = *reinterpret_cast<const uint4*>(kb + x * kPage * C::kBox + key * C::kBox + c * 16);
+                }
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                const int step = x * (C::kBox / 16) + h * 4 + w;
+                uint2 bq[NT];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) bq[nt] = q_s[(nt * C::kKSteps + step) * 32 + lane];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const uint32_t wa = w == 0 ? raw[j][0].x : w == 1 ? raw[j][0].y : w == 2 ? raw[j][0].z : raw[j][0].w;
+                  const uint32_t wb = w == 0 ? raw[j][1].x : w == 1 ? raw[j][1].y : w == 2 ? raw[j][1].z : raw[j][1].w;
+                  uint32_t a0, a1, a2, a3;
+                  decode4<E4M3>(wa, a0, a2);
+                  decode4<E4M3>(wb, a1, a3);
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) mma_f16(s[j][nt], a0, a1, a2, a3, bq[nt].x, bq[nt].y);
+                }
+              }
+            }
+        }
+        __syncwarp();
+        issue();  // K's slot is free
+        ++done;
+        // ------------------------------------------------------------ softmax: this thread's rows 2t, 2t+1
+        uint32_t pb[4][NT][2];  // P^T fragments
+        bool moved = false;
+        float alpha[NT][2];
+        const float unit_new = vs > 0.f ? fmaxf(vs, fmaxf(max_v, vs) * 9.094947e-13f) : unit_v;  // 2^-40: see below
+        const float p_scale = vs > 0.f ? vs / unit_new : 1.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float cf = qs_s[nt * 8 + 2 * t + x] * ks;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              s[j][nt][x] *= cf;
+              s[j][nt][2 + x] *= cf;
+            }
+            if (partial) {
+              const uint2 bits = bits_s[nt * 8 + 2 * t + x];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t w = j < 2 ? bits.x : bits.y;
+                if (!((w >> (16 * (j & 1) + g)) & 1u)) s[j][nt][x] = kNegInf;
+                if (!((w >> (16 * (j & 1) + 8 + g)) & 1u)) s[j][nt][2 + x] = kNegInf;
+              }
+            }
+          }
+          if (p.accumulate && row_base + nt * 8 + 2 * t < p.rows4) {
+            float* dst = p.score + ((int64_t)bh * cap + slot0 + g) * p.rows4 + row_base + nt * 8 + 2 * t;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              *reinterpret_cast<float2*>(dst + (int64_t)(16 * j) * p.rows4) = make_float2(s[j][nt][0], s[j][nt][1]);
+              *reinterpret_cast<float2*>(dst + (int64_t)(16 * j + 8) * p.rows4) = make_float2(s[j][nt][2], s[j][nt][3]);
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float mx = fmaxf(s[0][nt][x], s[0][nt][2 + x]);
+#pragma unroll
+            for (int j = 1; j < 4; ++j) mx = fmaxf(mx, fmaxf(s[j][nt][x], s[j][nt][2 + x]));
+#pragma unroll
+            for (int y = 4; y < 32; y <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
+            const float m_new = fmaxf(m[nt][x], mx - kPBias);
+            const float m_use = m_new == kNegInf ? 0.f : m_new;
+            alpha[nt][x] = ex2(m[nt][x] - m_use);
+            moved |= m_new != m[nt][x];
+            m[nt][x] = m_new;
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              s[j][nt][x] = ex2(s[j][nt][x] - m_use);
+              s[j][nt][2 + x] = ex2(s[j][nt][2 + x] - m_use);
+              sum += s[j][nt][x] + s[j][nt][2 + x];
+            }
+            l[nt][x] = fmaf(l[nt][x], alpha[nt][x], sum);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {  // keys 16 j + 2t, +1 and + 8, + 9 of row g, as the product reads them
+            pb[j][nt][0] = transpose8x8(pack_f16(s[j][nt][0] * p_scale, s[j][nt][1] * p_scale));
+            pb[j][nt][1] = transpose8x8(pack_f16(s[j][nt][2] * p_scale, s[j][nt][3] * p_scale));
+          }
+        }
+        // O moves to this block's maximum and V scale.  The V scale is a common factor of a block's codes, so
+        // O is held in units of the last block's; a block more than 2^40 below the largest one seen keeps to
+        // 2^-40 of that, its P scaled instead (O would overflow in ever smaller units).
+        const float fu = unit_v > 0.f ? unit_v / unit_new : 1.f;
+        max_v = fmaxf(max_v, vs);
+        unit_v = unit_new;
+        if (__any_sync(0xffffffffu, moved || fu != 1.f)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float f0 = alpha[nt][0] * fu, f1 = alpha[nt][1] * fu;
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) {
+              o[i][nt][0] *= f0;
+              o[i][nt][1] *= f1;
+              o[i][nt][2] *= f0;
+              o[i][nt][3] *= f1;
+            }
+          }
+        }
+        // ------------------------------------------------------------ O^T += V^T P^T
+        wait();
+        {
+          const uint8_t* vb = ring_p + (item + done) % kSlots * C::kSlotBytes;
+          const int valid = len - slot0;
+          constexpr int kWords = C::kBox / 32;  // 32-bit words of a row's piece that belongs to lane group g
+#pragma unroll
+          for (int x = 0; x < C::kBoxes; ++x)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t raw[4][kWords];  // keys 16 j + 2t, + 1, + 8, + 9
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const int key = 16 * j + 2 * t + (r & 1) + 8 * (r >> 1);
+                if constexpr (C::kBox == 128) {
+                  const uint4 v = *reinterpret_cast<const uint4*>(vb + x * kPage * 128 + key * 128 + ((g ^ (key & 7)) << 4));
+                  raw[r][0] = v.x;
+                  raw[r][1] = v.y;
+                  raw[r][2] = v.z;
+                  raw[r][3] = v.w;
+                } else {
+                  const uint2 v = *reinterpret_cast<const uint2*>(vb + key * 64 + (((g >> 1) ^ ((key >> 1) & 3)) << 4) + (g & 1) * 8);
+                  raw[r][0] = v.x;
+                  raw[r][1] = v.y;
+                }
+                if (partial && key >= valid) {  // slots never written may hold any bytes, a NaN's among them
+#pragma unroll
+                  for (int w = 0; w < kWords; ++w) raw[r][w] = 0;
+                }
+              }
+#pragma unroll
+              for (int w = 0; w < kWords; ++w) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {  // bytes 2u, 2u + 1: d rows of tile 2 w + u
+                  const uint32_t sel = u ? 0x7362u : 0x5140u;
+                  uint32_t a0, a1, a2, a3;
+                  decode4<E4M3>(__byte_perm(raw[0][w], raw[1][w], sel), a0, a1);
+                  decode4<E4M3>(__byte_perm(raw[2][w], raw[3][w], sel), a2, a3);
+                  const int tile = x * (C::kBox / 16) + 2 * w + u;
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) mma_f16(o[tile][nt], a0, a1, a2, a3, pb[j][nt][0], pb[j][nt][1]);
+                }
+              }
+            }
+        }
+        __syncwarp();
+        issue();
+        ++done;
+      }
+      if (!(flag & 2)) continue;  // goes on in the next list
+
+      // -------------------------------------------------- the segment's end: join the warps
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+          for (int y = 4; y < 32; y <<= 1) l[nt][x] += __shfl_xor_sync(0xffffffffu, l[nt][x], y);
+          if (g == 0) ml_s[warp * C::kRows + nt * 8 + 2 * t + x] = make_float2(m[nt][x], l[nt][x]);
+        }
+      __syncthreads();
+      if (sg + 1 < n_seg) store_q();  // every warp is done with the old rows
+      float mj[NT][2], lj[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float mm = kNegInf, ll = 0.f;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, ml_s[w * C::kRows + nt * 8 + 2 * t + x].x);
+          const float use = mm == kNegInf ? 0.f : mm;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            const float2 v = ml_s[w * C::kRows + nt * 8 + 2 * t + x];
+            ll += v.y * ex2(v.x - use);
+          }
+          mj[nt][x] = mm;
+          lj[nt][x] = ll;
+          const float f = ex2(m[nt][x] - use) * unit_v;
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i) {
+            o[i][nt][x] *= f;
+            o[i][nt][2 + x] *= f;
+          }
+        }
+#pragma unroll
+      for (int h = kWarps / 2; h > 0; h >>= 1) {
+        if (warp >= h && warp < 2 * h) {
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) tree[((warp - h) * C::kRegs + (i * NT + nt) * 4 + c) * 32 + lane] = o[i][nt][c];
+        }
+        __syncthreads();
+        if (warp < h) {
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) o[i][nt][c] += tree[(warp * C::kRegs + (i * NT + nt) * 4 + c) * 32 + lane];
+        }
+        __syncthreads();
+      }
+      if (warp == 0) {
+        const int nb = (len + kPage - 1) / kPage;
+        const int u0 = units[b] + hk * nb, u1 = u0 + nb;
+        const bool whole = u0 >= c0 && u1 <= c1;
+        const int64_t part = ((int64_t)work * 2 + (u0 > c0 ? 1 : 0)) * p.n_rows_pad;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int r = row_base + nt * 8 + 2 * t + x;
+            const float ll = lj[nt][x];
+            if (whole) {
+              if (r >= p.n_rows) continue;
+              const int h = hk * p.group + r / p.n_q, tq = r % p.n_q;
+              const float inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);  // (a NaN stays one)
+              __nv_bfloat16* dst = p.o + (((int64_t)b * p.n_q + tq) * p.H + h) * D;
+#pragma unroll
+              for (int i = 0; i < kTiles; i += 4) {  // tiles i .. i + 3: 8 consecutive d of this lane's piece
+                const int d = i / (C::kBox / 16) * C::kBox + g * (C::kBox / 8) + 2 * (i % (C::kBox / 16));
+                st_global_v4(dst + d, pack_bf16(o[i][nt][x] * inv, o[i][nt][2 + x] * inv),
+                             pack_bf16(o[i + 1][nt][x] * inv, o[i + 1][nt][2 + x] * inv),
+                             pack_bf16(o[i + 2][nt][x] * inv, o[i + 2][nt][2 + x] * inv),
+                             pack_bf16(o[i + 3][nt][x] * inv, o[i + 3][nt][2 + x] * inv));
+              }
+              if (g == 0) {
+                p.lse[((int64_t)b * p.H + h) * p.n_q + tq] = (mj[nt][x] + log2f(ll)) * kLn2;
+                if (p.accumulate) p.whole_ml[(int64_t)bh * p.n_rows_pad + r] = make_float2(mj[nt][x], ll);
+              }
+            } else {
+              float* dst = p.part_o + (part + r) * D;
+#pragma unroll
+              for (int i = 0; i < kTiles; i += 2) {
+                const int d = i / (C::kBox / 16) * C::kBox + g * (C::kBox / 8) + 2 * (i % (C::kBox / 16));
+                *reinterpret_cast<float4*>(dst + d) =
+                    make_float4(o[i][nt][x], o[i][nt][2 + x], o[i + 1][nt][x], o[i + 1][nt][2 + x]);
+              }
+              if (g == 0) p.part_ml[part + r] = make_float2(mj[nt][x], ll);
+            }
+          }
+      }
+    }
+    item += done;
+  }
+}
+
+// Second kernel.  The first B * H_kv * n_rows CTAs each join one row of a (sequence, head) that several runs
+// share; the others each add the softmax weights of kWeightSlots keys to the cache's, from the stored scores.
+constexpr int kJoinThreads = 128;
+constexpr int kWeightSlots = 512;
+constexpr int kMaxRows = 1024;
+
+struct Span {  // the runs that hold a (sequence, head)
+  int u0, first, last;  // last < first: no units
+};
+__device__ __forceinline__ Span span_of(const CacheAttnParams& p, int b, int hk) {
+  const int a = p.units[b], z = p.units[b + 1], nb = (z - a) / p.H_kv;
+  const int per = (p.units[p.B] + p.n_work - 1) / p.n_work;
+  Span s;
+  s.u0 = a + hk * nb;
+  s.first = nb ? s.u0 / per : 0;
+  s.last = nb ? (s.u0 + nb - 1) / per : -1;
+  return s;
+}
+__device__ __forceinline__ int64_t part_of(const CacheAttnParams& p, const Span& s, int c) {
+  const int per = (p.units[p.B] + p.n_work - 1) / p.n_work;
+  return ((int64_t)c * 2 + (s.u0 > c * per ? 1 : 0)) * p.n_rows_pad;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const CacheAttnParams p) {
+  __shared__ float2 ml[kMaxRows];
+  const int n_join = p.B * p.H_kv * p.n_rows;
+  if ((int)blockIdx.x < n_join) {
+    const int bh = blockIdx.x / p.n_rows, r = blockIdx.x % p.n_rows, b = bh / p.H_kv, hk = bh % p.H_kv;
+    const Span s = span_of(p, b, hk);
+    if (s.first == s.last) return;  // written by its one run
+    float m = kNegInf, l = 0.f;
+    for (int c = s.first; c <= s.last; ++c) m = fmaxf(m, p.part_ml[part_of(p, s, c) + r].x);
+    const float use = m == kNegInf ? 0.f : m;
+    for (int c = s.first; c <= s.last; ++c) {
+      const float2 v = p.part_ml[part_of(p, s, c) + r];
+      l += v.y * ex2(v.x - use);
+    }
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    const int h = hk * p.group + r / p.n_q, tq = r % p.n_q;
+    for (int d = threadIdx.x; d < D; d += kJoinThreads) {
+      float x = 0.f;
+      for (int c = s.first; c <= s.last; ++c) {
+        const int64_t at = part_of(p, s, c) + r;
+        x += p.part_o[at * D + d] * ex2(p.part_ml[at].x - use);
+      }
+      p.o[(((int64_t)b * p.n_q + tq) * p.H + h) * D + d] = __float2bfloat16_rn(x * inv);
+    }
+    if (threadIdx.x == 0) p.lse[((int64_t)b * p.H + h) * p.n_q + tq] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
+    return;
+  }
+  const int cap = p.max_pages * kPage, per_bh = (cap + kWeightSlots - 1) / kWeightSlots;
+  const int w = blockIdx.x - n_join, bh = w / per_bh, s0 = w % per_bh * kWeightSlots, b = bh / p.H_kv, hk = bh % p.H_kv;
+  const int len = min(max(__ldg(p.len + b), 0), cap);
+  if (s0 >= len) return;
+  const Span s = span_of(p, b, hk);
+  for (int r = threadIdx.x; r < p.rows4; r += kJoinThreads) {
+    float m = 0.f, l = 0.f;
+    if (r < p.n_rows) {
+      if (s.first == s.last) {
+        const float2 v = p.whole_ml[(int64_t)bh * p.n_rows_pad + r];
+        m = v.x;
+        l = v.y;
+      } else {
+        m = kNegInf;
+        for (int c = s.first; c <= s.last; ++c) m = fmaxf(m, p.part_ml[part_of(p, s, c) + r].x);
+        const float use = m == kNegInf ? 0.f : m;
+        for (int c = s.first; c <= s.last; ++c) {
+          const float2 v = p.part_ml[part_of(p, s, c) + r];
+          l += v.y * ex2(v.x - use);
+        }
+      }
+    }
+    ml[r] = make_float2(m == kNegInf ? 0.f : m, l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l));
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < kWeightSlots; i += kJoinThreads) {
+    const int slot = s0 + i;
+    if (slot >= len || !p.live[(int64_t)bh * p.max_pages + slot / kPage]) continue;
+    const float4* sc = reinterpret_cast<const float4*>(p.score + ((int64_t)bh * cap + slot) * p.rows4);
+    float x = 0.f;
+    for (int r = 0; r < p.rows4; r += 4) {
+      const float4 v = __ldg(sc + r / 4);
+      // rows behind the last one hold no score: their factor is 0 and their exponent finite
+      x += ex2(v.x - ml[r].x) * ml[r].y;
+      if (r + 1 < p.n_rows) x += ex2(v.y - ml[r + 1].x) * ml[r + 1].y;
+      if (r + 2 < p.n_rows) x += ex2(v.z - ml[r + 2].x) * ml[r + 2].y;
+      if (r + 3 < p.n_rows) x += ex2(v.w - ml[r + 3].x) * ml[r + 3].y;
+    }
+    p.weight[(int64_t)bh * cap + slot] += x;
+  }
+}
+
+// ------------------------------------------------------------------------------------------- host
+// Query rows a CTA holds: 8 for up to 8 rows, more where that spares reading the cache again (through L2)
+// for the next rows, as far as the accumulators fit the registers.
+int row_tiles(int D, int n_rows) {
+  const int most = D == 64 ? 4 : 2;
+  const int need = (n_rows + 7) / 8;
+  return need >= most ? most : need == 3 ? 4 : need;
+}
+
+struct Layout {
+  int nt, n_chunks, n_work, n_rows, n_rows_pad, rows4;
+  size_t units, part_o, part_ml, whole_ml, score, live, total;
+};
+
+Layout layout_of(const fm_kv_cache* c, const fm_cache_attn_args* a) {
+  Layout L;
+  const size_t bh = (size_t)c->B * c->H_kv;
+  L.n_rows = a->n_q * (a->H / c->H_kv);
+  L.nt = row_tiles(c->D, L.n_rows);
+  L.n_chunks = (L.n_rows + 8 * L.nt - 1) / (8 * L.nt);
+  L.n_rows_pad = L.n_chunks * 8 * L.nt;
+  L.rows4 = (L.n_rows + 3) / 4 * 4;
+  const int64_t most = (int64_t)bh * c->max_pages;
+  L.n_work = L.n_chunks >= kSMs ? 1 : kSMs / L.n_chunks;
+  if (L.n_work > most) L.n_work = (int)most;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t r = at;
+    at += (bytes + 255) / 256 * 256;
+    return r;
+  };
+  L.units = take((size_t)(c->B + 1) * 4);
+  L.part_o = take((size_t)L.n_work * 2 * L.n_rows_pad * c->D * 4);
+  L.part_ml = take((size_t)L.n_work * 2 * L.n_rows_pad * 8);
+  const bool acc = a->accumulate != 0;
+  L.whole_ml = take(acc ? bh * L.n_rows_pad * 8 : 0);
+  L.live = take(acc ? bh * c->max_pages : 0);
+  L.score = take(acc ? bh * c->max_pages * kPage * L.rows4 * 4 : 0);
+  L.total = at;
+  return L;
+}
+
+fm_status check_cache_attn(const fm_kv_cache* c, const fm_cache_attn_args* a) {
+  const fm_status st = check_cache(c);
+  if (st != FM_OK) return st;
+  if (!a || a->n_q < 1 || a->H < 1 || a->H > 65535 || a->H % c->H_kv) return FM_ERR_INVALID_ARG;
+  if (a->dtype != 0) return FM_ERR_UNSUPPORTED;
+  if (a->H / c->H_kv > 64 || a->n_q > kMaxRows || a->n_q * (a->H / c->H_kv) > kMaxRows) return FM_ERR_UNSUPPORTED;
+  if ((int64_t)c->B * a->H * a->n_q >= ((int64_t)1 << 30)) return FM_ERR_UNSUPPORTED;
+  if (!(a->scale > 0.f) || a->scale > 3.0e38f) return FM_ERR_INVALID_ARG;
+  if ((a->causal != 0 && a->causal != 1) || (a->accumulate != 0 && a->accumulate != 1)) return FM_ERR_INVALID_ARG;
+  if (a->accumulate && !c->weight) return FM_ERR_INVALID_ARG;
+  if (a->Hm == 0 ? a->n_k != 0 : ((a->Hm != 1 && a->Hm != a->H) || a->n_k < 1)) return FM_ERR_INVALID_ARG;
+  return FM_OK;
+}
+
+// Tensor map over a code pool: rows of D bytes (page, head, slot), boxes of 64 rows, 64- or 128-byte swizzle.
+bool encode_pool(CUtensorMap* map, const fm_kv_cache* c, const void* base) {
+  return encode_tmap_u8_rows(map, base, c->D, (uint64_t)c->n_pages * c->H_kv * kPage, kPage);
+}
+
+template <int D, int NT, bool E4M3>
+fm_status launch(const fm_kv_cache* c, const CacheAttnParams& p, cudaStream_t s) {
+  using C = CacheAttnCfg<D, NT>;
+  static_assert(C::kUnits + (kMaxCacheB + 1) * 4 + 1024 <= 227 * 1024, "shared memory exceeds the per-CTA limit");
+  CUtensorMap tk, tv;
+  if (!encode_pool(&tk, c, c->k_codes) || !encode_pool(&tv, c, c->v_codes)) return FM_ERR_CUDA;
+  constexpr int kMost = C::kUnits + (kMaxCacheB + 1) * 4 + 1024;
+  if (!smem_opt_in<cache_attn_kernel<D, NT, E4M3>>(kMost)) return FM_ERR_CUDA;
+  const int bytes = C::kUnits + (p.B + 1) * 4 + 1024;
+  cache_attn_kernel<D, NT, E4M3><<<p.n_work * p.n_chunks, C::kThreads, bytes, s>>>(tk, tv, p);
+  if (cudaGetLastError() != cudaSuccess) return FM_ERR_CUDA;
+  const int64_t bh = (int64_t)p.B * p.H_kv;
+  int64_t grid = bh * p.n_rows;
+  if (p.accumulate) grid += bh * ((p.max_pages * kPage + kWeightSlots - 1) / kWeightSlots);
+  cache_join_kernel<D><<<(unsigned)grid, kJoinThreads, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? FM_OK : FM_ERR_CUDA;
+}
+
+template <int D, bool E4M3>
+fm_status launch_nt(int nt, const fm_kv_cache* c, const CacheAttnParams& p, cudaStream_t s) {
+  if (nt == 1) return launch<D, 1, E4M3>(c, p, s);
+  if constexpr (D == 64) {
+    if (nt == 4) return launch<D, 4, E4M3>(c, p, s);
+  }
+  return launch<D, 2, E4M3>(c, p, s);
+}
+
+}  // namespace
+}  // namespace fm
+
+extern "C" {
+
+size_t fm_cache_attn_workspace_bytes(const fm_kv_cache* cache, const fm_cache_attn_args* a) {
+  return fm::check_cache_attn(cache, a) == FM_OK ? fm::layout_of(cache, a).total : 0;
+}
+
+fm_status fm_cache_attn(const fm_kv_cache* c, const fm_cache_attn_args* a, void* o, float* lse, void* ws,
+                        size_t ws_bytes, fm_stream_t stream) {
+  const fm_status st = fm::check_cache_attn(c, a);
+  if (st != FM_OK) return st;
+  bool vecs = false;
+  uintptr_t low = reinterpret_cast<uintptr_t>(a->len) | reinterpret_cast<uintptr_t>(a->row) | reinterpret_cast<uintptr_t>(lse);
+  for (int i = 0; i < 4; ++i) {
+    vecs = vecs || a->vec[i];
+    low |= reinterpret_cast<uintptr_t>(a->vec[i]);
+  }
+  if (!a->q || !a->len || !o || !lse || (low & 3)) return FM_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(a->q) | reinterpret_cast<uintptr_t>(o)) & 15) return FM_ERR_INVALID_ARG;
+  if (vecs && a->Hm == 0) return FM_ERR_INVALID_ARG;
+  if ((vecs || a->causal) && !a->row) return FM_ERR_INVALID_ARG;
+  const fm::Layout L = fm::layout_of(c, a);
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255) || ws_bytes < L.total) return FM_ERR_WORKSPACE;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  fm::CacheAttnParams p;
+  p.q = static_cast<const __nv_bfloat16*>(a->q);
+  p.len = a->len;
+  p.row = a->row;
+  for (int i = 0; i < 4; ++i) p.vec[i] = a->vec[i];
+  p.page_table = c->page_table;
+  p.k_scale = c->k_scale;
+  p.v_scale = c->v_scale;
+  p.pos = c->pos;
+  p.weight = c->weight;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.units = reinterpret_cast<int32_t*>(base + L.units);
+  p.part_o = reinterpret_cast<float*>(base + L.part_o);
+  p.part_ml = reinterpret_cast<float2*>(base + L.part_ml);
+  p.whole_ml = reinterpret_cast<float2*>(base + L.whole_ml);
+  p.score = reinterpret_cast<float*>(base + L.score);
+  p.live = base + L.live;
+  p.status = fm::device_status_ptr();
+  p.B = c->B;
+  p.H = a->H;
+  p.H_kv = c->H_kv;
+  p.n_q = a->n_q;
+  p.group = a->H / c->H_kv;
+  p.n_rows = L.n_rows;
+  p.n_rows_pad = L.n_rows_pad;
+  p.rows4 = L.rows4;
+  p.Hm = a->Hm;
+  p.n_k = a->n_k;
+  p.n_pages = c->n_pages;
+  p.max_pages = c->max_pages;
+  p.n_work = L.n_work;
+  p.n_chunks = L.n_chunks;
+  p.masked = vecs || a->causal;
+  p.causal = a->causal;
+  p.accumulate = a->accumulate;
+  p.scale_log2 = a->scale * fm::kLog2e;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  switch (c->D * 2 + c->code_type) {
+    case 128: return fm::launch_nt<64, false>(L.nt, c, p, s);
+    case 129: return fm::launch_nt<64, true>(L.nt, c, p, s);
+    case 256: return fm::launch_nt<128, false>(L.nt, c, p, s);
+    case 257: return fm::launch_nt<128, true>(L.nt, c, p, s);
+    case 512: return fm::launch_nt<256, false>(L.nt, c, p, s);
+    default: return fm::launch_nt<256, true>(L.nt, c, p, s);
+  }
+}
+
+}  // extern "C"

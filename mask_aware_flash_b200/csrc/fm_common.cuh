@@ -590,4 +590,5 @@ bool encode_tmap_bf16_4d(CUtensorMap* map, const void* base, uint64_t D, uint64_
                          uint32_t box_rows);
 bool encode_tmap_f32_4d(CUtensorMap* map, const void* base, uint64_t D, uint64_t H, uint64_t n, uint64_t B,
                         uint32_t box_rows);
+bool encode_tmap_u8_rows(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_rows);
 }  // namespace fm
