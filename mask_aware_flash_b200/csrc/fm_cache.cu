@@ -31,17 +31,18 @@ __device__ __forceinline__ T pick(T const (&a)[2], int which) {
   return which ? a[1] : a[0];
 }
 
-// Block-wide maximum of non-negative values; every thread gets it.  `red`: one float per warp.
+// Block-wide maximum of the bit patterns of non-negative floats (their order, with infinity and then NaN on top);
+// every thread gets it.  `red`: one word per warp; it may be used again after the next __syncthreads.
 template <int kThreads>
-__device__ __forceinline__ float block_max(float v, float* red) {
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, s));
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* red) {
+  v = __reduce_max_sync(0xffffffffu, v);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) v = fmaxf(v, red[w]);
+  for (int w = 0; w < kThreads / 32; ++w) v = max(v, red[w]);
   return v;
 }
+constexpr uint32_t kInfBits = 0x7F800000u;
 
 // ------------------------------------------------------------------------------------------ append
 struct AppendParams {
@@ -57,37 +58,73 @@ struct AppendParams {
   int n_new, H_kv, n_pages, max_pages;
 };
 
-// 16 consecutive elements as fp32
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&x)[16]) {
+// 16 consecutive elements as they lie in memory, and as fp32
+template <typename T>
+struct Raw16;
+template <>
+struct Raw16<__nv_bfloat16> {
+  uint4 v[2];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    v[0] = __ldg(reinterpret_cast<const uint4*>(p));
+    v[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+  }
+  // bit pattern (as fp32) of the largest |x|: both halves of a word at once
+  __device__ __forceinline__ uint32_t max_bits() const {
+    uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    for (int i = 0; i < 2; ++i) {
+      m = __vmaxu2(m, v[i].x & 0x7FFF7FFFu);
+      m = __vmaxu2(m, v[i].y & 0x7FFF7FFFu);
+      m = __vmaxu2(m, v[i].z & 0x7FFF7FFFu);
+      m = __vmaxu2(m, v[i].w & 0x7FFF7FFFu);
+    }
+    return max(m << 16, m & 0xFFFF0000u);
+  }
+  __device__ __forceinline__ void get(float (&x)[16]) const {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[8 * i + 2 * j] = bf16_lo(w[j]);
-      x[8 * i + 2 * j + 1] = bf16_hi(w[j]);
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[8 * i + 2 * j] = bf16_lo(w[j]);
+        x[8 * i + 2 * j + 1] = bf16_hi(w[j]);
+      }
     }
   }
-}
-__device__ __forceinline__ void load16(const float* p, float (&x)[16]) {
+};
+template <>
+struct Raw16<float> {
+  float4 v[4];
+  __device__ __forceinline__ void load(const float* p) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(p) + i);
-    x[4 * i] = v.x;
-    x[4 * i + 1] = v.y;
-    x[4 * i + 2] = v.z;
-    x[4 * i + 3] = v.w;
+    for (int i = 0; i < 4; ++i) v[i] = __ldg(reinterpret_cast<const float4*>(p) + i);
   }
-}
+  __device__ __forceinline__ uint32_t max_bits() const {
+    float x[16];
+    get(x);
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) m = max(m, __float_as_uint(x[j]) & 0x7FFFFFFFu);
+    return m;
+  }
+  __device__ __forceinline__ void get(float (&x)[16]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[4 * i] = v[i].x;
+      x[4 * i + 1] = v[i].y;
+      x[4 * i + 2] = v[i].z;
+      x[4 * i + 3] = v[i].w;
+    }
+  }
+};
 
-template <bool E4M3>
-__device__ __forceinline__ uint4 encode16(const float (&x)[16], float inv) {
+template <bool E4M3, bool kSafe>
+__device__ __forceinline__ uint4 encode16(const float (&x)[16], float f) {
   uint4 r;
-  r.x = encode4<E4M3>(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-  r.y = encode4<E4M3>(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
-  r.z = encode4<E4M3>(x[8] * inv, x[9] * inv, x[10] * inv, x[11] * inv);
-  r.w = encode4<E4M3>(x[12] * inv, x[13] * inv, x[14] * inv, x[15] * inv);
+  r.x = encode4<E4M3, kSafe>(x[0] * f, x[1] * f, x[2] * f, x[3] * f);
+  r.y = encode4<E4M3, kSafe>(x[4] * f, x[5] * f, x[6] * f, x[7] * f);
+  r.z = encode4<E4M3, kSafe>(x[8] * f, x[9] * f, x[10] * f, x[11] * f);
+  r.w = encode4<E4M3, kSafe>(x[12] * f, x[13] * f, x[14] * f, x[15] * f);
   return r;
 }
 template <bool E4M3>
@@ -108,7 +145,7 @@ __device__ __forceinline__ void decode16(const uint4& v, float (&x)[16]) {
 template <int D, typename T, bool E4M3>
 __global__ void __launch_bounds__(2 * D) append_kernel(const AppendParams p) {
   constexpr int kThreads = 2 * D, kPieces = D / 16;
-  __shared__ float red[kThreads / 32];
+  __shared__ uint32_t red[2][kThreads / 32];
   const int which = blockIdx.x & 1, hk = blockIdx.y, b = blockIdx.z;
   const int start = __ldg(p.start + b);
   const int count = p.count ? min(max(__ldg(p.count + b), 0), p.n_new) : p.n_new;
@@ -117,35 +154,52 @@ __global__ void __launch_bounds__(2 * D) append_kernel(const AppendParams p) {
   const int64_t t0 = (int64_t)block * kPage - start;  // token of the block's first slot (negative: older slots)
   if (t0 >= count || t0 + kPage <= 0) return;
   const int page = __ldg(p.page_table + (int64_t)b * p.max_pages + block);
-  if (page < 0 || page >= p.n_pages) return;
-  const int64_t at = (int64_t)page * p.H_kv + hk;
-  const float s_old = t0 < 0 ? pick(p.scale, which)[at] : 0.f;
-  float x[2][16];
+  Raw16<T> x[2];
   bool fresh[2];
-  float amax = 0.f;
+  uint32_t bits = 0;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int piece = threadIdx.x + i * kThreads;
     const int64_t t = t0 + piece / kPieces;
     fresh[i] = t >= 0 && t < count;
-    if (!fresh[i]) continue;
-    load16(static_cast<const T*>(pick(p.src, which)) + (((int64_t)b * p.n_new + t) * p.H_kv + hk) * D + piece % kPieces * 16, x[i]);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) amax = fmaxf(amax, finite_abs(x[i][j]));
+    if (fresh[i])
+      x[i].load(static_cast<const T*>(pick(p.src, which)) + (((int64_t)b * p.n_new + t) * p.H_kv + hk) * D +
+                piece % kPieces * 16);
   }
-  amax = block_max<kThreads>(amax, red);
-  const float s = fmaxf(s_old, scale_rule<E4M3>(amax));
+  if (page < 0 || page >= p.n_pages) return;
+  const int64_t at = (int64_t)page * p.H_kv + hk;
+  const float s_old = t0 < 0 ? pick(p.scale, which)[at] : 0.f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (fresh[i]) bits = max(bits, x[i].max_bits());
+  bits = block_max<kThreads>(bits, red[0]);
+  const bool safe = bits >= kInfBits;  // an infinity or a NaN is among the values: they do not count
+  if (safe) {
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (fresh[i]) {
+        float y[16];
+        x[i].get(y);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) amax = fmaxf(amax, finite_abs(y[j]));
+      }
+    bits = block_max<kThreads>(__float_as_uint(amax), red[1]);
+  }
+  const float s = fmaxf(s_old, scale_rule<E4M3>(__uint_as_float(bits)));
   const float inv = s > 0.f ? 1.f / s : 0.f;
   const bool grow = t0 < 0 && s != s_old;  // older codes move to the larger scale
   uint4* codes = reinterpret_cast<uint4*>(pick(p.codes, which) + at * (kPage * D));
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int piece = threadIdx.x + i * kThreads;
+    float y[16];
     if (fresh[i]) {
-      codes[piece] = encode16<E4M3>(x[i], inv);
+      x[i].get(y);
+      codes[piece] = safe ? encode16<E4M3, true>(y, inv) : encode16<E4M3, false>(y, inv);
     } else if (grow && t0 + piece / kPieces < 0) {
-      decode16<E4M3>(codes[piece], x[i]);
-      codes[piece] = encode16<E4M3>(x[i], s_old * inv);
+      decode16<E4M3>(codes[piece], y);
+      codes[piece] = encode16<E4M3, true>(y, s_old * inv);
     }
   }
   if (threadIdx.x == 0) pick(p.scale, which)[at] = s;
@@ -185,9 +239,10 @@ struct EvictParams {
   int32_t* dst_pos;
   const int32_t* len;
   int32_t* new_len;
-  int32_t* kept;    // ws: [B, H_kv, budget] source slots, ascending
+  int32_t* kept;    // ws: [B, H_kv, budget] the kept slots' rows (page * 64 + slot % 64; -1: no page), ascending slots
   int32_t* n_kept;  // ws: [B, H_kv]
   int H_kv, src_pages, dst_pages, src_max, dst_max, budget, recent;
+  int chunk;  // slots of a CTA of the selection (a multiple of 32)
 };
 
 // Unsigned key that orders weights as the selection does: larger weight, larger key; -0 equals +0;
@@ -198,143 +253,362 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;         // 11 bits a pass
+constexpr int kSelMaxKeys = 49152;  // keys a CTA can hold in shared memory
 
-// Exclusive prefix sum over the block of a pair packed into 64 bits; `total` gets the block's sum.
-__device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* red, uint64_t& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint64_t x = v;
-#pragma unroll
-  for (int s = 1; s < 32; s <<= 1) {
-    const uint64_t y = __shfl_up_sync(0xffffffffu, x, s);
-    if (lane >= s) x += y;
-  }
-  if (lane == 31) red[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    uint64_t w = red[lane];
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-      const uint64_t y = __shfl_up_sync(0xffffffffu, w, s);
-      if (lane >= s) w += y;
-    }
-    red[lane] = w;
-  }
-  __syncthreads();
-  total = red[31];
-  return x - v + (warp ? red[warp - 1] : 0);
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t ld_cluster(const uint32_t* p, uint32_t rank) {  // another CTA's shared memory
+  uint32_t v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\t"
+      "mapa.shared::cluster.u32 a, %1, %2;\n\t"
+      "ld.shared::cluster.u32 %0, [a];\n\t}"
+      : "=r"(v)
+      : "r"(smem_u32(p)), "r"(rank)
+      : "memory");
+  return v;
 }
 
-// One CTA per (head, sequence): the budget - recent largest weights of the older slots by a radix
-// selection (four passes of 8 bits over the keys, a 256-bin histogram in shared memory), then one
-// ordered pass that writes the kept slots ascending.
+struct SelSmem {
+  uint32_t hist[kBins];
+  uint32_t mine[kBins];   // totals over the cluster of this CTA's share of the bins
+  uint32_t share_total;   // their sum
+  uint32_t digit, left;   // the pass's result
+  uint32_t above, equal;  // of this CTA's slots
+  uint32_t first, last;   // its part of the kept list
+  uint32_t warp_above[kSelWarps], warp_equal[kSelWarps];
+  uint32_t scan[kSelWarps];
+};
+
+// The budget - recent largest weights of the older slots of one (head, sequence) by a radix selection, 11 bits of the
+// keys a pass, then one ordered pass that writes the kept slots ascending.  A cluster of CTAs shares the slots
+// (contiguous runs); histograms and counts are exchanged through distributed shared memory.  kHeld: the keys stay in
+// shared memory after the one read of the weights (else every pass reads them again).
+template <bool kHeld>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p) {
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t s_prefix, s_need;
-  __shared__ uint64_t red[32];
-  const int hk = blockIdx.x, b = blockIdx.y;
+  extern __shared__ uint32_t keys[];
+  __shared__ SelSmem sm;
+  const int rank = (int)cluster_rank(), size = (int)cluster_size();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int hk = blockIdx.y, b = blockIdx.z;
   const int64_t bh = (int64_t)b * p.H_kv + hk;
   const int n = min(max(__ldg(p.len + b), 0), p.src_max * kPage);
+  if (threadIdx.x == 0 && rank == 0) p.n_kept[bh] = min(n, p.budget);
   int32_t* kept = p.kept + bh * p.budget;
-  if (threadIdx.x == 0) p.n_kept[bh] = min(n, p.budget);
-  if (n <= p.budget) {
-    for (int i = threadIdx.x; i < n; i += kSelThreads) kept[i] = i;
+  const float* w = p.src_weight + bh * p.src_max * kPage;
+  const int32_t* pos = p.src_pos ? p.src_pos + bh * p.src_max * kPage : nullptr;
+  float* to_w = p.dst_weight ? p.dst_weight + bh * p.dst_max * kPage : nullptr;
+  int32_t* to_pos = p.dst_pos ? p.dst_pos + bh * p.dst_max * kPage : nullptr;
+  const int32_t* table = p.src_table + (int64_t)b * p.src_max;
+  // What the new cache takes of the slots from(first), from(first + step), ... for its slots first, first + step, ... < end:
+  // four at a time, so that their loads overlap.
+  auto keep = [&](int first, int end, int step, auto from) {
+    for (int to = first; to < end; to += 4 * step) {
+      int f[4], page[4], q[4];
+      float x[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) f[u] = to + u * step < end ? from(to + u * step) : -1;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        page[u] = f[u] >= 0 ? __ldg(table + f[u] / kPage) : -1;
+        x[u] = to_w && f[u] >= 0 ? __ldg(w + f[u]) : 0.f;
+        q[u] = to_pos && pos && f[u] >= 0 ? __ldg(pos + f[u]) : f[u];
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (f[u] >= 0) {
+          kept[to + u * step] = page[u] >= 0 && page[u] < p.src_pages ? page[u] * kPage + f[u] % kPage : -1;
+          if (to_w) to_w[to + u * step] = x[u];
+          if (to_pos) to_pos[to + u * step] = q[u];
+        }
+    }
+  };
+  if (n <= p.budget) {  // (the same for every CTA of the cluster)
+    keep(rank * kSelThreads + threadIdx.x, n, size * kSelThreads, [](int i) { return i; });
     return;
   }
   const int older = n - p.recent, want = p.budget - p.recent;  // older > want >= 0
-  const float* w = p.src_weight + bh * p.src_max * kPage;
+  keep(want + rank * kSelThreads + threadIdx.x, p.budget, size * kSelThreads, [&](int i) { return older + i - want; });
+  if (want == 0) return;
+  // this CTA's run of slots; a length below the table's leaves CTAs fewer slots, not other ones without any
+  const int run = min(p.chunk, (((older + size - 1) / size) + 31) / 32 * 32);
+  const int i0 = min(rank * run, older), mine = min(i0 + run, older) - i0;
+  auto key = [&](int i) { return kHeld ? keys[i] : weight_key(__ldg(w + i0 + i)); };
+  if (kHeld) {
+    for (int i = threadIdx.x; i < mine; i += 8 * kSelThreads) {
+      float x[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) x[u] = i + u * kSelThreads < mine ? __ldg(w + i0 + i + u * kSelThreads) : 0.f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (i + u * kSelThreads < mine) keys[i + u * kSelThreads] = weight_key(x[u]);
+    }
+  }
   uint32_t prefix = 0, need = want;
-  if (want > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = threadIdx.x; i < 256; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
-      for (int i = threadIdx.x; i < older; i += kSelThreads) {
-        const uint32_t k = weight_key(__ldg(w + i));
-        if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255u], 1u);
-      }
+  const int share = kBins / size;  // bins whose totals this CTA adds up
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const uint32_t digits = pass == 2 ? 1024u : (uint32_t)kBins;
+    for (int i = threadIdx.x; i < kBins; i += kSelThreads) sm.hist[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < mine; i += kSelThreads) {
+      const uint32_t k = key(i);
+      if (pass == 0 || (k >> (pass == 1 ? 21 : 10)) == (prefix >> (pass == 1 ? 21 : 10)))
+        atomicAdd(&sm.hist[(k >> shift) & (digits - 1)], 1u);
+    }
+    if (size > 1) cluster_sync_all();
+    else __syncthreads();
+    // totals of this CTA's bins, and their sum
+    uint32_t sum = 0;
+    for (int i = threadIdx.x; i < share; i += kSelThreads) {
+      uint32_t t = 0;
+      if (size > 1)
+        for (int c = 0; c < size; ++c) t += ld_cluster(&sm.hist[rank * share + i], c);
+      else
+        t = sm.hist[i];
+      sm.mine[i] = t;
+      sum += t;
+    }
+    uint32_t left = need;
+    int c = 0;
+    if (size > 1) {  // the share in which the count from the top reaches `need`
+      sum = __reduce_add_sync(0xffffffffu, sum);
+      if (lane == 0) sm.scan[warp] = sum;
       __syncthreads();
       if (threadIdx.x == 0) {
-        uint32_t left = need;
-        int d = 255;
-        while (hist[d] < left) left -= hist[d--];
-        s_prefix = prefix | ((uint32_t)d << shift);
-        s_need = left;
+        uint32_t t = 0;
+        for (int i = 0; i < kSelWarps; ++i) t += sm.scan[i];
+        sm.share_total = t;
       }
+      cluster_sync_all();
+      const uint32_t t = lane < size ? ld_cluster(&sm.share_total, lane) : 0;
+      for (c = size - 1; c > 0; --c) {
+        const uint32_t tc = __shfl_sync(0xffffffffu, t, c);
+        if (tc >= left) break;
+        left -= tc;
+      }
+    } else {
       __syncthreads();
-      prefix = s_prefix;
-      need = s_need;
+    }
+    // the bin in it: thread i takes the i-th run of bins from the top
+    {
+      const int per = share > kSelThreads ? share / kSelThreads : 1;
+      const int top = share - 1 - (int)threadIdx.x * per;
+      uint32_t t[kBins / kSelThreads], mine_sum = 0;
+#pragma unroll
+      for (int j = 0; j < kBins / kSelThreads; ++j) {
+        t[j] = j < per && top - j >= 0 ? (size > 1 ? ld_cluster(&sm.mine[top - j], c) : sm.mine[top - j]) : 0;
+        mine_sum += t[j];
+      }
+      uint32_t x = mine_sum;
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, x, s);
+        if (lane >= s) x += y;
+      }
+      if (lane == 31) sm.scan[warp] = x;
+      __syncthreads();
+      uint32_t before = x - mine_sum;
+      for (int i = 0; i < warp; ++i) before += sm.scan[i];
+      if (before < left && before + mine_sum >= left) {  // one thread
+#pragma unroll
+        for (int j = 0; j < kBins / kSelThreads; ++j) {
+          if (before < left && before + t[j] >= left) {
+            sm.digit = (uint32_t)(c * share + top - j);
+            sm.left = left - before;
+          }
+          before += t[j];
+        }
+      }
+    }
+    if (size > 1) cluster_sync_all();  // (nobody changes its bins while another reads them)
+    else __syncthreads();
+    prefix |= sm.digit << shift;
+    need = sm.left;
+  }
+  // prefix: the key of the last one taken; `need` of the keys equal to it are taken, lowest slots first.
+  // Counts of each warp's run of slots, of the CTA, and of the CTAs before it
+  const int per_warp = ((run + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
+  const int a0 = min(warp * per_warp, mine), a1 = min(a0 + per_warp, mine);
+  uint32_t above = 0, equal = 0;
+  for (int i = a0 + lane; i < a1; i += 32) {
+    const uint32_t k = key(i);
+    above += k > prefix;
+    equal += k == prefix;
+  }
+  above = __reduce_add_sync(0xffffffffu, above);
+  equal = __reduce_add_sync(0xffffffffu, equal);
+  if (lane == 0) {
+    sm.warp_above[warp] = above;
+    sm.warp_equal[warp] = equal;
+  }
+  __syncthreads();
+  above = equal = 0;
+  for (int i = 0; i < warp; ++i) {
+    above += sm.warp_above[i];
+    equal += sm.warp_equal[i];
+  }
+  if (size > 1) {
+    if (threadIdx.x == kSelThreads - 1) {
+      sm.above = above + sm.warp_above[kSelWarps - 1];
+      sm.equal = equal + sm.warp_equal[kSelWarps - 1];
+    }
+    cluster_sync_all();
+    for (int c = 0; c < rank; ++c) {
+      above += ld_cluster(&sm.above, c);
+      equal += ld_cluster(&sm.equal, c);
     }
   }
-  // prefix: the key of the last one taken; `need` of the keys equal to it are taken, lowest slots first
-  const int per = (older + kSelThreads - 1) / kSelThreads;
-  const int i0 = min((int)threadIdx.x * per, older), i1 = min(i0 + per, older);
-  uint64_t mine = 0;  // above | equal << 32
-  if (want > 0)
-    for (int i = i0; i < i1; ++i) {
-      const uint32_t k = weight_key(__ldg(w + i));
-      mine += k > prefix ? 1ull : (k == prefix ? (1ull << 32) : 0ull);
-    }
-  uint64_t total;
-  uint64_t before = block_scan(mine, red, total);
-  if (want > 0)
-    for (int i = i0; i < i1; ++i) {
-      const uint32_t k = weight_key(__ldg(w + i));
-      const uint32_t above = (uint32_t)before, equal = (uint32_t)(before >> 32);
-      if (k > prefix || (k == prefix && equal < need)) kept[above + min(equal, need)] = i;
-      before += k > prefix ? 1ull : (k == prefix ? (1ull << 32) : 0ull);
-    }
-  for (int i = threadIdx.x; i < p.recent; i += kSelThreads) kept[want + i] = older + i;
+  // the kept slots in order, then (in parallel again) what the new cache takes of each
+  if (threadIdx.x == 0) sm.first = above + min(equal, need);
+  const uint32_t below = (1u << lane) - 1u;
+  for (int i = a0; i < a1; i += 32) {
+    const uint32_t k = i + lane < a1 ? key(i + lane) : 0;
+    const bool in = i + lane < a1;
+    const uint32_t ba = __ballot_sync(0xffffffffu, in && k > prefix), be = __ballot_sync(0xffffffffu, in && k == prefix);
+    const uint32_t before_a = above + __popc(ba & below), before_e = equal + __popc(be & below);
+    if (in && (k > prefix || (k == prefix && before_e < need))) kept[before_a + min(before_e, need)] = i0 + i + lane;
+    above += __popc(ba);
+    equal += __popc(be);
+  }
+  if (threadIdx.x == kSelThreads - 1) sm.last = above + min(equal, need);
+  __syncthreads();
+  keep((int)sm.first + threadIdx.x, (int)sm.last, kSelThreads, [&](int i) { return kept[i]; });
+  if (size > 1) cluster_sync_all();  // no CTA leaves while its counts are read
 }
 
-// One CTA per (dst block, K or V, head, sequence): gathers the kept slots' codes, re-quantises them
-// together (values stay in registers) and writes the block once.
+// Byte permutation whose selectors with the top bit set give the sign of a byte, eight times.
+template <uint32_t kSel>
+__device__ __forceinline__ uint32_t bytes_signed(uint32_t w) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(w), "n"(kSel));
+  return r;
+}
+
+// The largest magnitude of four times four codes, as a number in code units.  int8: the bytes go to 16-bit pairs with their
+// signs, a running maximum and minimum of each; e4m3: magnitudes are ordered as their 7-bit patterns.
+template <bool E4M3>
+__device__ __forceinline__ float max_code(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if constexpr (E4M3) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __vmaxu2(m, __vmaxu2(w[i] & 0x007F007Fu, (w[i] >> 8) & 0x007F007Fu));
+    float y[4];
+    decode4f<E4M3>(max(m & 0xFFu, m >> 16), y);
+    return y[0];
+  } else {
+    uint32_t hi = 0, lo = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a = bytes_signed<0x9180>(w[i]), b = bytes_signed<0xB3A2>(w[i]);
+      hi = __vmaxs2(hi, __vmaxs2(a, b));
+      lo = __vmins2(lo, __vmins2(a, b));
+    }
+    const int top = max((int)(int16_t)(hi & 0xFFFFu), (int)(int16_t)(hi >> 16));
+    const int low = min((int)(int16_t)(lo & 0xFFFFu), (int)(int16_t)(lo >> 16));
+    return (float)max(top, -low);
+  }
+}
+
+// One CTA per (dst block, head, sequence): gathers the kept slots' K and V codes, re-quantises each together (codes stay
+// in registers) and writes the block once.  Bound by memory: the kept rows are D bytes each, two dependent loads away.
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(2 * D) compact_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(2 * D, 1024 / (2 * D)) compact_kernel(const EvictParams p) {
   constexpr int kThreads = 2 * D, kPieces = D / 16;
-  __shared__ float red[kThreads / 32];
-  const int which = blockIdx.x & 1, block = blockIdx.x >> 1, hk = blockIdx.y, b = blockIdx.z;
+  __shared__ uint32_t red[2][kThreads / 32];
+  const int block = blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
   const int64_t bh = (int64_t)b * p.H_kv + hk;
   const int n = __ldg(p.n_kept + bh);
-  if (block == 0 && which == 0 && hk == 0 && threadIdx.x == 0) p.new_len[b] = n;
-  if (block * kPage >= n) return;
-  const int32_t* kept = p.kept + bh * p.budget;
-  if (which == 0 && threadIdx.x < kPage && block * kPage + (int)threadIdx.x < n) {
-    const int to = block * kPage + threadIdx.x, from = __ldg(kept + to);
-    const int64_t src = bh * p.src_max * kPage + from, dst = bh * p.dst_max * kPage + to;
-    if (p.dst_weight) p.dst_weight[dst] = __ldg(p.src_weight + src);
-    if (p.dst_pos) p.dst_pos[dst] = p.src_pos ? __ldg(p.src_pos + src) : from;
-  }
   const int page = __ldg(p.dst_table + (int64_t)b * p.dst_max + block);
-  if (page < 0 || page >= p.dst_pages) return;
-  float x[2][16];
-  float amax = 0.f;
+  int row[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {  // (entries behind the n-th are there, without a meaning)
+    const int to = block * kPage + (threadIdx.x + i * kThreads) / kPieces;
+    row[i] = to < p.budget ? __ldg(p.kept + bh * p.budget + to) : -1;
+  }
+  if (block == 0 && hk == 0 && threadIdx.x == 0) p.new_len[b] = n;
+  if (block * kPage >= n || page < 0 || page >= p.dst_pages) return;
+  uint4 raw[2][2];
+  float scale[2][2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int piece = threadIdx.x + i * kThreads, to = block * kPage + piece / kPieces;
+    const int piece = threadIdx.x + i * kThreads;
+    if (block * kPage + piece / kPieces >= n) row[i] = -1;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) x[i][j] = 0.f;
-    if (to >= n) continue;
-    const int from = __ldg(kept + to);
-    const int sp = __ldg(p.src_table + (int64_t)b * p.src_max + from / kPage);
-    if (sp < 0 || sp >= p.src_pages) continue;
-    const int64_t at = (int64_t)sp * p.H_kv + hk;
-    const float s = __ldg(pick(p.src_scale, which) + at);
-    decode16<E4M3>(__ldg(reinterpret_cast<const uint4*>(pick(p.src_codes, which) + (at * kPage + from % kPage) * D) + piece % kPieces),
-                   x[i]);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      x[i][j] *= s;
-      amax = fmaxf(amax, finite_abs(x[i][j]));
+    for (int x = 0; x < 2; ++x) {
+      raw[x][i] = make_uint4(0, 0, 0, 0);  // (code 0 of both formats)
+      scale[x][i] = 0.f;
+      if (row[i] >= 0) {
+        const int64_t at = (int64_t)(row[i] / kPage) * p.H_kv + hk;
+        scale[x][i] = __ldg(p.src_scale[x] + at);
+        raw[x][i] = __ldg(reinterpret_cast<const uint4*>(p.src_codes[x] + (at * kPage + row[i] % kPage) * D) + piece % kPieces);
+      }
     }
   }
-  amax = block_max<kThreads>(amax, red);
-  const float s = scale_rule<E4M3>(amax);
-  const float inv = s > 0.f ? 1.f / s : 0.f;
-  const int64_t at = (int64_t)page * p.H_kv + hk;
-  uint4* codes = reinterpret_cast<uint4*>(pick(p.dst_codes, which) + at * (kPage * D));
+  uint32_t bits[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) codes[threadIdx.x + i * kThreads] = encode16<E4M3>(x[i], inv);
-  if (threadIdx.x == 0) pick(p.dst_scale, which)[at] = s;
+  for (int x = 0; x < 2; ++x) {
+    bits[x] = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      bits[x] = max(bits[x], __float_as_uint(fabsf(max_code<E4M3>(raw[x][i]) * scale[x][i])));
+    bits[x] = __reduce_max_sync(0xffffffffu, bits[x]);
+    if ((threadIdx.x & 31) == 0) red[x][threadIdx.x >> 5] = bits[x];
+  }
+  __syncthreads();
+  const int64_t at = (int64_t)page * p.H_kv + hk;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) bits[x] = max(bits[x], red[x][w]);
+    // (a product that overflows, from scales no append writes: the largest finite scale, its codes saturate)
+    const bool safe = bits[x] >= kInfBits;
+    const float s = scale_rule<E4M3>(__uint_as_float(min(bits[x], kInfBits - 1)));
+    const float inv = s > 0.f ? 1.f / s : 0.f;
+    uint4* codes = reinterpret_cast<uint4*>(p.dst_codes[x] + at * (kPage * D));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float y[16];
+      decode16<E4M3>(raw[x][i], y);
+      const float f = scale[x][i] * inv;
+      codes[threadIdx.x + i * kThreads] = safe ? encode16<E4M3, true>(y, f) : encode16<E4M3, false>(y, f);
+    }
+    if (threadIdx.x == 0) p.dst_scale[x][at] = s;
+  }
+}
+
+template <bool kHeld>
+cudaError_t launch_select(const EvictParams& p, int B, int cluster, int keys, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cluster, p.H_kv, B);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = kHeld ? keys * 4 : 0;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = cluster;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (kHeld && !smem_opt_in<select_kernel<true>>(kSelMaxKeys * 4)) return cudaErrorInvalidValue;
+  return cudaLaunchKernelEx(&cfg, select_kernel<kHeld>, p);
 }
 
 size_t evict_n_kept_offset(const fm_kv_cache* src, int32_t budget) {
@@ -426,8 +700,15 @@ fm_status fm_cache_evict(const fm_kv_cache* src, const fm_kv_cache* dst, const i
   p.budget = budget;
   p.recent = recent;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  fm::select_kernel<<<dim3(src->H_kv, src->B), fm::kSelThreads, 0, s>>>(p);
-  const dim3 grid(2 * (unsigned)((budget + fm::kPage - 1) / fm::kPage), src->H_kv, src->B);
+  // The CTAs of a selection: one per 4096 slots of the table, as far as a cluster goes and the SMs are not full yet.
+  const int64_t slots = (int64_t)src->max_pages * fm::kPage, lists = (int64_t)src->B * src->H_kv;
+  int cluster = 1;
+  while (cluster < 8 && slots > 4096 * (int64_t)cluster && lists * cluster * 2 <= 2 * 148) cluster *= 2;
+  p.chunk = (int)(((slots + cluster - 1) / cluster + 31) / 32 * 32);
+  const bool held = p.chunk <= fm::kSelMaxKeys;
+  const cudaError_t e = held ? fm::launch_select<true>(p, src->B, cluster, p.chunk, s) : fm::launch_select<false>(p, src->B, cluster, 0, s);
+  if (e != cudaSuccess) return FM_ERR_CUDA;
+  const dim3 grid((unsigned)((budget + fm::kPage - 1) / fm::kPage), src->H_kv, src->B);
   if (src->D == 64)
     src->code_type ? fm::compact_kernel<64, true><<<grid, 128, 0, s>>>(p) : fm::compact_kernel<64, false><<<grid, 128, 0, s>>>(p);
   else if (src->D == 128)

@@ -37,14 +37,18 @@ __device__ __forceinline__ float finite_abs(float x) {
 
 // Four values (already divided by their scale) -> four codes, the first in the low byte.  Rounded to
 // nearest even, as both formats hold no more: half a step of the block's scale (int8) or half a unit of
-// e4m3's 4-bit significand.
-template <bool E4M3>
+// e4m3's 4-bit significand.  kSafe: any values; otherwise finite ones within the format's range (the values
+// of a block without infinities and NaN, whose scale the rule above gives).  int8 in range: adding 1.5 * 2^23
+// rounds to an integer whose two's complement low byte is the low byte of the sum's word.
+template <bool E4M3, bool kSafe>
 __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
   float x[4] = {a, b, c, d};
+  if constexpr (kSafe) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[i] = x[i] == x[i] ? x[i] : 0.f;
-    x[i] = fminf(fmaxf(x[i], -code_max<E4M3>()), code_max<E4M3>());
+    for (int i = 0; i < 4; ++i) {
+      x[i] = x[i] == x[i] ? x[i] : 0.f;
+      x[i] = fminf(fmaxf(x[i], -code_max<E4M3>()), code_max<E4M3>());
+    }
   }
   if constexpr (E4M3) {
     uint32_t r;
@@ -56,10 +60,10 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
         : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]));
     return r;
   } else {
-    uint32_t r = 0;
+    uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r |= ((uint32_t)__float2int_rn(x[i]) & 0xFFu) << (8 * i);
-    return r;
+    for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(x[i] + 12582912.f);
+    return __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
   }
 }
 
