@@ -253,9 +253,8 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kBins = 2048;         // 11 bits a pass
+constexpr int kDigitBits = 11;      // a pass
+constexpr int kBins = 1 << kDigitBits;
 constexpr int kSelMaxKeys = 49152;  // keys a CTA can hold in shared memory
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -283,25 +282,41 @@ __device__ __forceinline__ uint32_t ld_cluster(const uint32_t* p, uint32_t rank)
   return v;
 }
 
-struct SelSmem {
-  uint32_t hist[kBins];
-  uint32_t mine[kBins];   // totals over the cluster of this CTA's share of the bins
-  uint32_t share_total;   // their sum
-  uint32_t digit, left;   // the pass's result
-  uint32_t above, equal;  // of this CTA's slots
-  uint32_t first, last;   // its part of the kept list
-  uint32_t warp_above[kSelWarps], warp_equal[kSelWarps];
-  uint32_t scan[kSelWarps];
-};
+__device__ __forceinline__ uint4 ld_cluster4(const uint32_t* p, uint32_t rank) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\t"
+      "mapa.shared::cluster.u32 a, %4, %5;\n\t"
+      "ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [a];\n\t}"
+      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+      : "r"(smem_u32(p)), "r"(rank)
+      : "memory");
+  return v;
+}
 
-// The budget - recent largest weights of the older slots of one (head, sequence) by a radix selection, 11 bits of the
-// keys a pass, then one ordered pass that writes the kept slots ascending.  A cluster of CTAs shares the slots
+struct SelSmem {
+  uint32_t hist[2][kBins];  // of this CTA's slots: passes alternate, so that the others may still read the last one's
+  uint32_t digit, left;     // the pass's result: its digit, how many of the keys with it are taken,
+  uint32_t all;             // whether those are all
+  uint32_t lowest, highest;
+  uint32_t above, equal;    // of this CTA's slots
+  uint32_t first, last;     // its part of the kept list
+  uint32_t warp_a[32], warp_b[32];
+};
+// Sum of v[0 .. n) for n <= 32, by every lane of a warp.
+__device__ __forceinline__ uint32_t sum_before(const uint32_t* v, int n, int lane) {
+  return __reduce_add_sync(0xffffffffu, lane < n ? v[lane] : 0u);
+}
+
+// The budget - recent largest weights of the older slots of one (head, sequence) by a radix selection, up to 11 bits
+// of the keys a pass, then one ordered pass that writes the kept slots ascending.  A cluster of CTAs shares the slots
 // (contiguous runs); histograms and counts are exchanged through distributed shared memory.  kHeld: the keys stay in
 // shared memory after the one read of the weights (else every pass reads them again).
-template <bool kHeld>
+template <bool kHeld, int kSelThreads>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p) {
+  constexpr int kSelWarps = kSelThreads / 32;
   extern __shared__ uint32_t keys[];
-  __shared__ SelSmem sm;
+  __shared__ __align__(16) SelSmem sm;
   const int rank = (int)cluster_rank(), size = (int)cluster_size();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int hk = blockIdx.y, b = blockIdx.z;
@@ -348,137 +363,154 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
   const int run = min(p.chunk, (((older + size - 1) / size) + 31) / 32 * 32);
   const int i0 = min(rank * run, older), mine = min(i0 + run, older) - i0;
   auto key = [&](int i) { return kHeld ? keys[i] : weight_key(__ldg(w + i0 + i)); };
-  if (kHeld) {
-    for (int i = threadIdx.x; i < mine; i += 8 * kSelThreads) {
-      float x[8];
+  // The range of the keys: digits are taken of key - lowest, from the highest bit that occurs, so that a pass tells as many
+  // keys apart as its bins can (of weights within a few octaves, the top bits of the key itself would fill a few bins).
+  uint32_t lowest = 0xFFFFFFFFu, highest = 0;
+  for (int i = threadIdx.x; i < mine; i += 8 * kSelThreads) {
+    float x[8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) x[u] = i + u * kSelThreads < mine ? __ldg(w + i0 + i + u * kSelThreads) : 0.f;
+    for (int u = 0; u < 8; ++u) x[u] = i + u * kSelThreads < mine ? __ldg(w + i0 + i + u * kSelThreads) : 0.f;
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
-        if (i + u * kSelThreads < mine) keys[i + u * kSelThreads] = weight_key(x[u]);
-    }
+    for (int u = 0; u < 8; ++u)
+      if (i + u * kSelThreads < mine) {
+        const uint32_t k = weight_key(x[u]);
+        if (kHeld) keys[i + u * kSelThreads] = k;
+        lowest = min(lowest, k);
+        highest = max(highest, k);
+      }
   }
-  uint32_t prefix = 0, need = want;
-  const int share = kBins / size;  // bins whose totals this CTA adds up
-#pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    const uint32_t digits = pass == 2 ? 1024u : (uint32_t)kBins;
-    for (int i = threadIdx.x; i < kBins; i += kSelThreads) sm.hist[i] = 0;
+  lowest = __reduce_min_sync(0xffffffffu, lowest);
+  highest = __reduce_max_sync(0xffffffffu, highest);
+  if (lane == 0) {
+    sm.warp_a[warp] = lowest;
+    sm.warp_b[warp] = highest;
+  }
+  __syncthreads();
+  lowest = __reduce_min_sync(0xffffffffu, sm.warp_a[lane % kSelWarps]);
+  highest = __reduce_max_sync(0xffffffffu, sm.warp_b[lane % kSelWarps]);
+  if (size > 1) {
+    if (threadIdx.x == 0) {
+      sm.lowest = lowest;
+      sm.highest = highest;
+    }
+    cluster_sync_all();
+    lowest = __reduce_min_sync(0xffffffffu, ld_cluster(&sm.lowest, lane % size));
+    highest = __reduce_max_sync(0xffffffffu, ld_cluster(&sm.highest, lane % size));
+  } else {
     __syncthreads();
-    for (int i = threadIdx.x; i < mine; i += kSelThreads) {
-      const uint32_t k = key(i);
-      if (pass == 0 || (k >> (pass == 1 ? 21 : 10)) == (prefix >> (pass == 1 ? 21 : 10)))
-        atomicAdd(&sm.hist[(k >> shift) & (digits - 1)], 1u);
+  }
+  // prefix: the digits found so far of the last key that is taken; `need`: how many are taken of the keys that share them
+  uint32_t prefix = 0, need = want;
+  int shift = 32 - __clz((int)(highest - lowest)), above_shift = 32;
+  uint32_t* hist = sm.hist[0];
+  for (bool more = shift > 0; more; hist = hist == sm.hist[0] ? sm.hist[1] : sm.hist[0]) {
+    above_shift = shift;
+    shift = max(shift - kDigitBits, 0);
+    for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i - lane < mine; i += 4 * kSelThreads) {
+      uint32_t k[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) k[u] = i + u * kSelThreads < mine ? key(i + u * kSelThreads) - lowest : 0;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bool in = i + u * kSelThreads < mine &&
+                        (above_shift == 32 ? 0u : k[u] >> above_shift) == (above_shift == 32 ? 0u : prefix >> above_shift);
+        const uint32_t d = (k[u] >> shift) & ((1u << (above_shift - shift)) - 1u), who = __ballot_sync(0xffffffffu, in);
+        if (who == 0) continue;
+        const int leader = __ffs(who) - 1;
+        const uint32_t d_leader = __shfl_sync(0xffffffffu, d, leader);  // (by every lane: not behind the && below)
+        const uint32_t same = __ballot_sync(0xffffffffu, in && d == d_leader);
+        if (same == who) {  // all the same (zeros, say): one addition for the warp
+          if (lane == leader) atomicAdd(&hist[d], (uint32_t)__popc(who));
+        } else if (in) {
+          atomicAdd(&hist[d], 1u);
+        }
+      }
     }
     if (size > 1) cluster_sync_all();
     else __syncthreads();
-    // totals of this CTA's bins, and their sum
-    uint32_t sum = 0;
-    for (int i = threadIdx.x; i < share; i += kSelThreads) {
-      uint32_t t = 0;
-      if (size > 1)
-        for (int c = 0; c < size; ++c) t += ld_cluster(&sm.hist[rank * share + i], c);
-      else
-        t = sm.hist[i];
-      sm.mine[i] = t;
-      sum += t;
-    }
-    uint32_t left = need;
-    int c = 0;
-    if (size > 1) {  // the share in which the count from the top reaches `need`
-      sum = __reduce_add_sync(0xffffffffu, sum);
-      if (lane == 0) sm.scan[warp] = sum;
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        uint32_t t = 0;
-        for (int i = 0; i < kSelWarps; ++i) t += sm.scan[i];
-        sm.share_total = t;
-      }
-      cluster_sync_all();
-      const uint32_t t = lane < size ? ld_cluster(&sm.share_total, lane) : 0;
-      for (c = size - 1; c > 0; --c) {
-        const uint32_t tc = __shfl_sync(0xffffffffu, t, c);
-        if (tc >= left) break;
-        left -= tc;
-      }
-    } else {
-      __syncthreads();
-    }
-    // the bin in it: thread i takes the i-th run of bins from the top
+    // The digit at which the count from the top reaches `need`: every CTA adds up the whole histogram, thread i the i-th
+    // four bins from the top.
     {
-      const int per = share > kSelThreads ? share / kSelThreads : 1;
-      const int top = share - 1 - (int)threadIdx.x * per;
-      uint32_t t[kBins / kSelThreads], mine_sum = 0;
-#pragma unroll
-      for (int j = 0; j < kBins / kSelThreads; ++j) {
-        t[j] = j < per && top - j >= 0 ? (size > 1 ? ld_cluster(&sm.mine[top - j], c) : sm.mine[top - j]) : 0;
-        mine_sum += t[j];
-      }
-      uint32_t x = mine_sum;
+      constexpr int kQuads = kBins / 4;
+      const int quad = kQuads - 1 - (int)threadIdx.x;
+      uint32_t t[4] = {0, 0, 0, 0};
+      if (quad >= 0)
+        for (int c = 0; c < size; ++c) {
+          const uint4 v = ld_cluster4(hist + 4 * quad, c);
+          t[0] += v.w;
+          t[1] += v.z;
+          t[2] += v.y;
+          t[3] += v.x;
+        }
+      const uint32_t own = t[0] + t[1] + t[2] + t[3];
+      uint32_t x = own;
 #pragma unroll
       for (int s = 1; s < 32; s <<= 1) {
         const uint32_t y = __shfl_up_sync(0xffffffffu, x, s);
         if (lane >= s) x += y;
       }
-      if (lane == 31) sm.scan[warp] = x;
+      if (lane == 31) sm.warp_a[warp] = x;
       __syncthreads();
-      uint32_t before = x - mine_sum;
-      for (int i = 0; i < warp; ++i) before += sm.scan[i];
-      if (before < left && before + mine_sum >= left) {  // one thread
+      uint32_t before = x - own + sum_before(sm.warp_a, warp, lane);
+      if (before < need && before + own >= need) {  // one thread
 #pragma unroll
-        for (int j = 0; j < kBins / kSelThreads; ++j) {
-          if (before < left && before + t[j] >= left) {
-            sm.digit = (uint32_t)(c * share + top - j);
-            sm.left = left - before;
+        for (int j = 0; j < 4; ++j) {
+          if (before < need && before + t[j] >= need) {
+            sm.digit = (uint32_t)(4 * quad + 3 - j);
+            sm.left = need - before;
+            sm.all = t[j] == need - before;
           }
           before += t[j];
         }
       }
+      __syncthreads();
     }
-    if (size > 1) cluster_sync_all();  // (nobody changes its bins while another reads them)
-    else __syncthreads();
     prefix |= sm.digit << shift;
     need = sm.left;
+    more = shift > 0 && !sm.all;  // all the keys with these digits are taken: the rest does not matter
   }
-  // prefix: the key of the last one taken; `need` of the keys equal to it are taken, lowest slots first.
+  auto rank_of = [&](int i) { return (key(i) - lowest) >> shift; };
+  prefix >>= shift;
+  // Keys above the prefix are taken, and `need` of those that share it, lowest slots first.
   // Counts of each warp's run of slots, of the CTA, and of the CTAs before it
   const int per_warp = ((run + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
   const int a0 = min(warp * per_warp, mine), a1 = min(a0 + per_warp, mine);
   uint32_t above = 0, equal = 0;
+#pragma unroll 4
   for (int i = a0 + lane; i < a1; i += 32) {
-    const uint32_t k = key(i);
+    const uint32_t k = rank_of(i);
     above += k > prefix;
     equal += k == prefix;
   }
   above = __reduce_add_sync(0xffffffffu, above);
   equal = __reduce_add_sync(0xffffffffu, equal);
   if (lane == 0) {
-    sm.warp_above[warp] = above;
-    sm.warp_equal[warp] = equal;
+    sm.warp_a[warp] = above;
+    sm.warp_b[warp] = equal;
   }
   __syncthreads();
-  above = equal = 0;
-  for (int i = 0; i < warp; ++i) {
-    above += sm.warp_above[i];
-    equal += sm.warp_equal[i];
+  if (size > 1 && warp == kSelWarps - 1) {
+    const uint32_t a = sum_before(sm.warp_a, kSelWarps, lane), e = sum_before(sm.warp_b, kSelWarps, lane);
+    if (lane == 0) {
+      sm.above = a;
+      sm.equal = e;
+    }
   }
+  above = sum_before(sm.warp_a, warp, lane);
+  equal = sum_before(sm.warp_b, warp, lane);
   if (size > 1) {
-    if (threadIdx.x == kSelThreads - 1) {
-      sm.above = above + sm.warp_above[kSelWarps - 1];
-      sm.equal = equal + sm.warp_equal[kSelWarps - 1];
-    }
     cluster_sync_all();
-    for (int c = 0; c < rank; ++c) {
-      above += ld_cluster(&sm.above, c);
-      equal += ld_cluster(&sm.equal, c);
-    }
+    above += __reduce_add_sync(0xffffffffu, lane < rank ? ld_cluster(&sm.above, lane) : 0u);
+    equal += __reduce_add_sync(0xffffffffu, lane < rank ? ld_cluster(&sm.equal, lane) : 0u);
   }
   // the kept slots in order, then (in parallel again) what the new cache takes of each
   if (threadIdx.x == 0) sm.first = above + min(equal, need);
   const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 4
   for (int i = a0; i < a1; i += 32) {
-    const uint32_t k = i + lane < a1 ? key(i + lane) : 0;
+    const uint32_t k = i + lane < a1 ? rank_of(i + lane) : 0;
     const bool in = i + lane < a1;
     const uint32_t ba = __ballot_sync(0xffffffffu, in && k > prefix), be = __ballot_sync(0xffffffffu, in && k == prefix);
     const uint32_t before_a = above + __popc(ba & below), before_e = equal + __popc(be & below);
@@ -593,12 +625,12 @@ __global__ void __launch_bounds__(2 * D, 1024 / (2 * D)) compact_kernel(const Ev
   }
 }
 
-template <bool kHeld>
-cudaError_t launch_select(const EvictParams& p, int B, int cluster, int keys, cudaStream_t s) {
+template <bool kHeld, int kThreads>
+cudaError_t launch_select(const EvictParams& p, int B, int cluster, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cluster, p.H_kv, B);
-  cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = kHeld ? keys * 4 : 0;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kHeld ? p.chunk * 4 : 0;
   cfg.stream = s;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -607,8 +639,8 @@ cudaError_t launch_select(const EvictParams& p, int B, int cluster, int keys, cu
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (kHeld && !smem_opt_in<select_kernel<true>>(kSelMaxKeys * 4)) return cudaErrorInvalidValue;
-  return cudaLaunchKernelEx(&cfg, select_kernel<kHeld>, p);
+  if (kHeld && !smem_opt_in<select_kernel<kHeld, kThreads>>(kSelMaxKeys * 4)) return cudaErrorInvalidValue;
+  return cudaLaunchKernelEx(&cfg, select_kernel<kHeld, kThreads>, p);
 }
 
 size_t evict_n_kept_offset(const fm_kv_cache* src, int32_t budget) {
@@ -706,7 +738,10 @@ fm_status fm_cache_evict(const fm_kv_cache* src, const fm_kv_cache* dst, const i
   while (cluster < 8 && slots > 4096 * (int64_t)cluster && lists * cluster * 2 <= 2 * 148) cluster *= 2;
   p.chunk = (int)(((slots + cluster - 1) / cluster + 31) / 32 * 32);
   const bool held = p.chunk <= fm::kSelMaxKeys;
-  const cudaError_t e = held ? fm::launch_select<true>(p, src->B, cluster, p.chunk, s) : fm::launch_select<false>(p, src->B, cluster, 0, s);
+  // 1024 threads a CTA where there is one CTA per SM at most, 512 where two share one
+  const bool wide = lists * cluster <= 148;
+  const cudaError_t e = held ? (wide ? fm::launch_select<true, 1024>(p, src->B, cluster, s) : fm::launch_select<true, 512>(p, src->B, cluster, s))
+                             : fm::launch_select<false, 1024>(p, src->B, cluster, s);
   if (e != cudaSuccess) return FM_ERR_CUDA;
   const dim3 grid((unsigned)((budget + fm::kPage - 1) / fm::kPage), src->H_kv, src->B);
   if (src->D == 64)
