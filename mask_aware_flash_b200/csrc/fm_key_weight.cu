@@ -2,14 +2,17 @@
 //
 //   weight_j = sum over heads h of the group, rows i of  exp(scale q_i.k_j - LSE_i)   [unmasked pairs]
 //
-// One key tile of 128 keys and K/V head per CTA (or per cluster of CTAs that share its work): the tile's K stays
-// in shared memory, the query tiles of its column lists (skip tiles never loaded) stream past it, head by head:
+// The work is cut into (key tile of 128 keys, K/V head): its K stays in shared memory, the query tiles of its column
+// lists (skip tiles never loaded) stream past it, head by head:
 //   S^T = K Q^T  (tcgen05, M = 128 keys, N = 128 queries) -> one of four TMEM buffers
 // so a thread holds one key: its sum stays in registers, its mask bounds too, and the interval test is a word of
-// bits per 32 queries.  Per score there is one exponential against 2 D flops of the tensor core: for D = 128 the
-// exponentials bound the kernel (16384 per tile at 16 per clock on the MUFU unit = 1024 clocks, against 512 of
-// the product).
-// Warps 0-3 / 4-7 take the even / odd query tiles, warp 8 issues the TMA loads, warp 9 the MMAs.
+// bits per 32 queries.  One CTA per SM works through a fixed share of the key tiles, longest lists first, and the
+// copies and products of the next key tile start while the last one is still being summed.  Where there are too few
+// key tiles for the SMs a cluster of CTAs shares each one's query tiles and adds up through distributed shared memory.
+// Per score there is one exponential against 2 D flops of the tensor core: for D = 128 the MUFU unit alone would take
+// 1024 clocks for a tile's 16384 (16 a clock) against 512 of the product, so a part of them goes to the FMA pipe.
+// Four warpgroups take the query tiles in turn (so that one's waits hide behind the others' exponentials), one warp lists
+// the items and issues the TMA loads, one issues the MMAs.
 #include "fm_common.cuh"
 
 namespace fm {
@@ -18,8 +21,13 @@ fm_status check_attn_args(const fm_attn_args* a, const fm_mask_meta* meta, const
 namespace {
 
 constexpr int kTile = 128;
-constexpr int kThreads = 320;
-constexpr int kBufs = 4;  // TMEM score buffers of 128 columns
+constexpr int kGroups = 4;    // warpgroups of sums
+constexpr int kThreads = kGroups * 128 + 64;
+constexpr int kListWarp = kGroups * 4, kMmaWarp = kListWarp + 1;
+constexpr int kSMs = 148;
+constexpr int kPolyEvery = 4;  // one score pair in kPolyEvery takes the polynomial instead of the MUFU unit
+constexpr int kBufs = kGroups;  // TMEM score buffers of 128 columns, one per warpgroup
+constexpr int kRing = 16;  // listed items
 constexpr float kNegInf = -__builtin_huge_valf();
 
 struct KeyWeightParams {
@@ -32,24 +40,30 @@ struct KeyWeightParams {
   int64_t weight_stride;
   int* status;
   int H, Hm, H_kv, q_per_kv, n_q, n_k, T_q, T_k, accumulate;
+  int n_work, n_bh, group;  // key tiles of all heads; B * H_kv; how many of those are dispatched together
   float scale_log2;
 };
 
 template <int D>
 struct KeyWeightSmem {
   static constexpr int kTileBytes = kTile * D * 2;
-  static constexpr int kStages = D == 256 ? 2 : D == 128 ? 5 : 8;  // query tiles in flight
+  static constexpr int kKBufs = D == 256 ? 1 : 2;                  // key tiles held
+  static constexpr int kStages = D == 256 ? 2 : D == 128 ? 4 : 8;  // query tiles in flight
   static constexpr int kK = 0;
-  static constexpr int kQ = kK + kTileBytes;
-  static constexpr int kLse = kQ + kStages * kTileBytes;  // [2 warpgroups][2][128] -log2 LSE
-  static constexpr int kSum = kLse + 2 * 2 * kTile * 4;   // [128] sums of the second warpgroup / of the CTA
-  static constexpr int kBar = kSum + kTile * 4;
-  enum { K_FULL, Q_FULL, Q_EMPTY = Q_FULL + kStages, S_FULL = Q_EMPTY + kStages, S_EMPTY = S_FULL + kBufs,
-         DRAIN = S_EMPTY + kBufs, kNumBars };
-  static constexpr int kMisc = kBar + kNumBars * 8;  // [0] TMEM base, [1] abort flag, [2] zero
+  static constexpr int kQ = kK + kKBufs * kTileBytes;
+  static constexpr int kLse = kQ + kStages * kTileBytes;     // [warpgroups][2][128] -log2 LSE
+  static constexpr int kSum = kLse + kGroups * 2 * kTile * 4;  // [2][warpgroups - 1][128] sums; [0][0]: of the CTA
+  static constexpr int kItems = kSum + 2 * (kGroups - 1) * kTile * 4;  // int4 ring of the listed items
+  static constexpr int kBar = kItems + kRing * 16;
+  enum { K_FULL, K_EMPTY = K_FULL + kKBufs, Q_FULL = K_EMPTY + kKBufs, Q_EMPTY = Q_FULL + kStages,
+         S_FULL = Q_EMPTY + kStages, S_EMPTY = S_FULL + kBufs, ITEM = S_EMPTY + kBufs, ITEM_FREE = ITEM + kRing,
+         LSE_FULL = ITEM_FREE + kRing, SUM_FULL = LSE_FULL + 2 * kGroups, SUM_EMPTY = SUM_FULL + 2, DRAIN = SUM_EMPTY + 2, kNumBars };
+  static constexpr int kMisc = kBar + kNumBars * 8;  // [0] TMEM base, [1] abort flag, [2] zero, [3] an LSE was a NaN
   static constexpr int kBytes = kMisc + 16;
   static constexpr int kAlloc = kBytes + 1024;
 };
+// An item: .x query-tile entry (qt << 1 | partial), .y query head of the group and flags, .z key tile, .w b << 16 | hk.
+constexpr int kFirst = 1 << 8, kLast = 2 << 8, kEmpty = 4 << 8, kEnd = 8 << 8;  // of the key tile; no query tile; no item
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -103,6 +117,68 @@ struct ItemWalk {
   }
 };
 
+// 2^x for a pair on the FMA and integer pipes, as exp2_poly2 but with the degree-5 minimax polynomial (relative error
+// 2.4e-7, a fourth of the MUFU unit's ulps more): the weights are fp32 results.  x <= 127; below -125 it gives 2^-125.
+constexpr float kExp2W0 = 1.000000119e+00f, kExp2W1 = 6.931469440e-01f, kExp2W2 = 2.402212024e-01f,
+                kExp2W3 = 5.550713092e-02f, kExp2W4 = 9.675540961e-03f, kExp2W5 = 1.327647245e-03f;
+__device__ __forceinline__ uint64_t exp2_poly5(uint64_t x2) {
+  constexpr float kRound = 12582912.0f;  // 1.5 * 2^23
+  const uint64_t xc = f2pack(fmaxf(f2lo(x2), -125.f), fmaxf(f2hi(x2), -125.f));
+  const uint64_t t2 = add2(xc, f2pack(kRound, kRound));
+  const uint64_t r2 = add2(t2, f2pack(-kRound, -kRound));
+  const uint64_t f2 = fma2(r2, f2pack(-1.f, -1.f), xc);
+  uint64_t q2 = fma2(f2, f2pack(kExp2W5, kExp2W5), f2pack(kExp2W4, kExp2W4));
+  q2 = fma2(q2, f2, f2pack(kExp2W3, kExp2W3));
+  q2 = fma2(q2, f2, f2pack(kExp2W2, kExp2W2));
+  q2 = fma2(q2, f2, f2pack(kExp2W1, kExp2W1));
+  q2 = fma2(q2, f2, f2pack(kExp2W0, kExp2W0));
+  const uint32_t lo = (uint32_t)q2 + ((uint32_t)t2 << 23);
+  const uint32_t hi = (uint32_t)(q2 >> 32) + ((uint32_t)(t2 >> 32) << 23);
+  return ((uint64_t)hi << 32) | lo;
+}
+
+// Adds the weights of 32 scores to the four running pairs; bit i of `masked`: query i does not see the key.  nl: -LSE of the
+// queries in log2 units.  kPoly: one pair in kPolyEvery goes to the FMA pipe (not once a row's LSE was a NaN, which the
+// polynomial would not pass on).
+template <bool kPoly>
+__device__ __forceinline__ void add_block(uint32_t (&s)[32], const float* nl, uint64_t sc2, uint32_t masked, uint64_t (&acc)[4]) {
+#pragma unroll
+  for (int c = 0; c < 32; c += 4) {
+    const float4 v = *reinterpret_cast<const float4*>(nl + c);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int i = c + 2 * u;
+      const uint64_t x = fma2(f2pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), sc2, u ? f2pack(v.z, v.w) : f2pack(v.x, v.y));
+      if (kPoly && (i / 2) % kPolyEvery == 0) {
+        const uint64_t y = exp2_poly5(x);
+        s[i] = (uint32_t)y;
+        s[i + 1] = (uint32_t)(y >> 32);
+      } else {
+        s[i] = __float_as_uint(ex2(f2lo(x)));
+        s[i + 1] = __float_as_uint(ex2(f2hi(x)));
+      }
+    }
+  }
+  if (__any_sync(0xffffffffu, masked != 0u)) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c) s[c] = ((masked >> c) & 1u) ? 0u : s[c];
+  }
+#pragma unroll
+  for (int c = 0; c < 32; c += 8)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) acc[u] = add2(acc[u], f2pack(__uint_as_float(s[c + 2 * u]), __uint_as_float(s[c + 2 * u + 1])));
+}
+
+// The key tile and head of piece of work `w`: groups of heads, in each the key tiles by rank (longest lists first).
+__device__ __forceinline__ void work_of(const KeyWeightParams& p, int w, int& bh, int& kt) {
+  const int per_group = p.group * p.T_k, grp = w / per_group, first = grp * p.group;
+  const int heads = min(p.group, p.n_bh - first), in = w - grp * per_group;
+  bh = first + in % heads;
+  const int b = bh / p.H_kv, hk = bh % p.H_kv;
+  const int64_t bhm = (int64_t)b * p.Hm + (p.Hm == 1 ? 0 : hk * p.q_per_kv);
+  kt = __ldg(p.order + bhm * p.T_k + in / heads);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     key_weight_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -113,34 +189,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = smem_base_1024(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank(), step = (int)cluster_size();
-  const int hk = blockIdx.y, b = blockIdx.z;
-  const int64_t bhm0 = (int64_t)b * p.Hm + (p.Hm == 1 ? 0 : hk * p.q_per_kv);
-  const int kt = __ldg(p.order + bhm0 * p.T_k + blockIdx.x / step);
-
-  ItemWalk walk;
-  walk.count = p.col_count + bhm0 * p.T_k + kt;
-  walk.entries = p.col_entries + (bhm0 * p.T_k + kt) * p.T_q;
-  walk.head_count = p.Hm == 1 ? 0 : p.T_k;
-  walk.head_entries = p.Hm == 1 ? 0 : (int64_t)p.T_k * p.T_q;
-  walk.heads = p.q_per_kv;
+  const int work0 = blockIdx.x / step, work_step = gridDim.x / step;
 
   const uint32_t bar0 = smem_u32(smem + S::kBar);
   auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + S::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
   const volatile int* never = reinterpret_cast<const volatile int*>(misc + 2);
+  volatile uint32_t* misc_v = misc;
   const uint32_t k_s = smem_u32(smem + S::kK), q_s = smem_u32(smem + S::kQ);
   float* lse_s = reinterpret_cast<float*>(smem + S::kLse);
   float* sum_s = reinterpret_cast<float*>(smem + S::kSum);
+  int4* items = reinterpret_cast<int4*>(smem + S::kItems);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kNumBars; ++i) mbar_init(bar(i), 1);
     for (int i = 0; i < kBufs; ++i) mbar_init(bar(S::S_EMPTY + i), kTile);
+    for (int i = 0; i < kRing; ++i) mbar_init(bar(S::ITEM_FREE + i), 4 * kGroups + 1);  // every warp of sums and the MMA role
+    for (int i = 0; i < 2 * kGroups; ++i) mbar_init(bar(S::LSE_FULL + i), 4);  // a warpgroup's warps
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(S::SUM_FULL + i), 4 * (kGroups - 1));
+      mbar_init(bar(S::SUM_EMPTY + i), 4);
+    }
     *abort_flag = 0;
-    misc[2] = 0;
+    misc[2] = misc[3] = 0;
     fence_barrier_init();
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_k);
   }
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(misc), 512);
     tmem_relinquish();
   }
@@ -148,62 +225,115 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = misc[0];
-  float sum = 0.f;
+  float sum = 0.f;    // of this thread's key (the last key tile's stays for the cluster's exchange)
+  int64_t key_at = -1;  // where it goes
 
-  if (warp == 8) {
-    // ------------------------------------------------------------ load role
+  if (warp == kListWarp) {
+    // ------------------------------------------------------- list and load role
     if (lane == 0) {
-      int hg, entry;
-      walk.start(rank);
+      int it = 0, qi = 0, wk = 0;  // items, query tiles and key tiles so far
       bool ok = true;
-      int i = 0;
-      for (; walk.get(hg, entry); ++i, walk.at += step) {
-        if (i == 0) {
-          mbar_arrive_expect_tx(bar(S::K_FULL), S::kTileBytes);
-          for (int c = 0; c < kAtoms; ++c) tma_load_4d(k_s + c * 16384, &tm_k, bar(S::K_FULL), c * 64, hk, kt * kTile, b);
-        }
-        const int st = i % S::kStages;
-        if (i >= S::kStages && !mbar_wait(bar(S::Q_EMPTY + st), (i / S::kStages - 1) & 1, abort_flag)) {
+      auto push = [&](int entry, int hg_flags, int kt, int b_hk) {
+        if (it >= kRing && !mbar_wait(bar(S::ITEM_FREE + it % kRing), (it / kRing - 1) & 1, abort_flag)) {
           ok = false;
-          break;
+          return;
         }
-        mbar_arrive_expect_tx(bar(S::Q_FULL + st), S::kTileBytes);
-        for (int c = 0; c < kAtoms; ++c)
-          tma_load_4d(q_s + st * S::kTileBytes + c * 16384, &tm_q, bar(S::Q_FULL + st), c * 64, hk * p.q_per_kv + hg,
-                      (entry >> 1) * kTile, b);
+        items[it % kRing] = make_int4(entry, hg_flags, kt, b_hk);
+        mbar_arrive(bar(S::ITEM + it % kRing));
+        ++it;
+      };
+      int bh = 0, kt = 0;
+      if (work0 < p.n_work) work_of(p, work0, bh, kt);
+      for (int w = work0; ok && w < p.n_work; w += work_step) {
+        int bh_next = 0, kt_next = 0;
+        if (w + work_step < p.n_work) work_of(p, w + work_step, bh_next, kt_next);  // (in flight until it is used)
+        const int b = bh / p.H_kv, hk = bh % p.H_kv;
+        const int b_hk = (int)((uint32_t)b << 16 | (uint32_t)hk);
+        const int64_t bhm0 = (int64_t)b * p.Hm + (p.Hm == 1 ? 0 : hk * p.q_per_kv);
+        ItemWalk walk;
+        walk.count = p.col_count + bhm0 * p.T_k + kt;
+        walk.entries = p.col_entries + (bhm0 * p.T_k + kt) * p.T_q;
+        walk.head_count = p.Hm == 1 ? 0 : p.T_k;
+        walk.head_entries = p.Hm == 1 ? 0 : (int64_t)p.T_k * p.T_q;
+        walk.heads = p.q_per_kv;
+        walk.start(rank);
+        int hg, entry;
+        bool more = walk.get(hg, entry);
+        if (!more) push(0, kEmpty | kLast, kt, b_hk);
+        for (bool first = true; ok && more; first = false) {
+          const int cur_hg = hg, cur = entry;
+          walk.at += step;
+          more = walk.get(hg, entry);  // (the next entry, in flight during this one's copies)
+          if (first) {
+            const int kb = wk % S::kKBufs;
+            if (wk >= S::kKBufs && !mbar_wait(bar(S::K_EMPTY + kb), (wk / S::kKBufs - 1) & 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(bar(S::K_FULL + kb), S::kTileBytes);
+            for (int c = 0; c < kAtoms; ++c)
+              tma_load_4d(k_s + kb * S::kTileBytes + c * 16384, &tm_k, bar(S::K_FULL + kb), c * 64, hk, kt * kTile, b);
+            ++wk;
+          }
+          const int st = qi % S::kStages;
+          if (qi >= S::kStages && !mbar_wait(bar(S::Q_EMPTY + st), (qi / S::kStages - 1) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(bar(S::Q_FULL + st), S::kTileBytes);
+          for (int c = 0; c < kAtoms; ++c)
+            tma_load_4d(q_s + st * S::kTileBytes + c * 16384, &tm_q, bar(S::Q_FULL + st), c * 64,
+                        hk * p.q_per_kv + cur_hg, (cur >> 1) * kTile, b);
+          ++qi;
+          push(cur, cur_hg | (first ? kFirst : 0) | (more ? 0 : kLast), kt, b_hk);
+        }
+        bh = bh_next;
+        kt = kt_next;
       }
+      if (ok) push(0, kEnd, 0, 0);
       if (!ok) record_failure(p.status, abort_flag, 61);
       // the copies in flight land before this role ends (a consumer that gave up may leave some unread)
-      if (i > 0) mbar_wait(bar(S::K_FULL), 0, never);
-      for (int x = max(i - S::kStages, 0); x < i; ++x) mbar_wait(bar(S::Q_FULL + x % S::kStages), (x / S::kStages) & 1, never);
+      for (int x = max(wk - S::kKBufs, 0); x < wk; ++x) mbar_wait(bar(S::K_FULL + x % S::kKBufs), (x / S::kKBufs) & 1, never);
+      for (int x = max(qi - S::kStages, 0); x < qi; ++x) mbar_wait(bar(S::Q_FULL + x % S::kStages), (x / S::kStages) & 1, never);
     }
-  } else if (warp == 9) {
+  } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------- MMA role
     if (lane == 0) {
       constexpr uint32_t kIdesc = idesc_bf16(128, 128, false, false);
       constexpr uint32_t kHi = desc_hi(1024);
       const uint32_t lo_k = desc_lo(k_s, 16), lo_q = desc_lo(q_s, 16);
-      int hg, entry;
-      walk.start(rank);
       bool ok = true;
-      int i = 0;
-      for (; walk.get(hg, entry); ++i, walk.at += step) {
-        const int st = i % S::kStages, buf = i % kBufs;
-        if ((i == 0 && !mbar_wait(bar(S::K_FULL), 0, abort_flag)) ||
-            !mbar_wait(bar(S::Q_FULL + st), (i / S::kStages) & 1, abort_flag) ||
-            (i >= kBufs && !mbar_wait(bar(S::S_EMPTY + buf), (i / kBufs - 1) & 1, abort_flag))) {
+      int qi = 0, wk = 0;
+      for (int it = 0;; ++it) {
+        if (!mbar_wait(bar(S::ITEM + it % kRing), (it / kRing) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const int flags = items[it % kRing].y;
+        mbar_arrive(bar(S::ITEM_FREE + it % kRing));
+        if (flags & kEnd) break;
+        if (flags & kEmpty) continue;
+        const int st = qi % S::kStages, buf = qi % kBufs, kb = wk % S::kKBufs;
+        if (((flags & kFirst) && !mbar_wait(bar(S::K_FULL + kb), (wk / S::kKBufs) & 1, abort_flag)) ||
+            !mbar_wait(bar(S::Q_FULL + st), (qi / S::kStages) & 1, abort_flag) ||
+            (qi >= kBufs && !mbar_wait(bar(S::S_EMPTY + buf), (qi / kBufs - 1) & 1, abort_flag))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t qa = lo_q + st * (S::kTileBytes >> 4);
+        const uint32_t qa = lo_q + st * (S::kTileBytes >> 4), ka = lo_k + kb * (S::kTileBytes >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-          umma_ss_w(tmem + buf * 128, lo_k + off, kHi, qa + off, kHi, kIdesc, k > 0 ? 1u : 0u);
+          umma_ss_w(tmem + buf * 128, ka + off, kHi, qa + off, kHi, kIdesc, k > 0 ? 1u : 0u);
         }
         umma_commit(bar(S::Q_EMPTY + st));
         umma_commit(bar(S::S_FULL + buf));
+        ++qi;
+        if (flags & kLast) {
+          umma_commit(bar(S::K_EMPTY + kb));
+          ++wk;
+        }
       }
       if (!ok) record_failure(p.status, abort_flag, 62);
       umma_commit(bar(S::DRAIN));  // every MMA has finished before TMEM is released
@@ -212,94 +342,110 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ------------------------------------------------------- exponentials and sums: one key per thread
     const int wg = warp >> 2, r = threadIdx.x & 127;
-    const int key = kt * kTile + r;
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
     float* my_lse = lse_s + wg * 2 * kTile;
     const uint64_t sc2 = f2pack(p.scale_log2, p.scale_log2);
     uint64_t acc[4] = {0, 0, 0, 0};
-    int at_head = -1;
+    int at_head = -1, ends = 0;
     int32_t lts = 0, lte = 0, uts = 0, ute = 0;
-    walk.start(rank);
-    int hg, entry;
     bool ok = true;
-    for (int i = 0; walk.get(hg, entry); ++i, walk.at += step) {
-      if ((i & 1) != wg) continue;
-      const int qt = entry >> 1, q0 = qt * kTile, buf = i % kBufs, lb = (i >> 1) & 1;
-      const bool ragged = q0 + kTile > p.n_q, partial = (entry & 1) || ragged;
-      // -LSE in log2 units, -inf for rows that see no key and rows past n_q (their p is 0)
-      {
-        const int row = q0 + r;
-        const float x = row < p.n_q ? __ldg(p.lse + ((int64_t)b * p.H + hk * p.q_per_kv + hg) * p.n_q + row) : kNegInf;
-        my_lse[lb * kTile + r] = x == kNegInf ? kNegInf : -x * 1.4426950408889634f;
-      }
-      if (partial && hg != at_head) {  // this key's bounds
-        const int64_t at = (bhm0 + (p.Hm == 1 ? 0 : hg)) * p.n_k + key;
-        const bool in = key < p.n_k;
-        lts = in && p.vec[0] ? __ldg(p.vec[0] + at) : p.n_q;
-        lte = in && p.vec[1] ? __ldg(p.vec[1] + at) : p.n_q;
-        uts = in && p.vec[2] ? __ldg(p.vec[2] + at) : 0;
-        ute = in && p.vec[3] ? __ldg(p.vec[3] + at) : 0;
-        at_head = hg;
-      }
-      named_bar_sync(1 + wg, 128);  // the values are there; the pair before last has been read
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(S::S_FULL + buf), (i / kBufs) & 1, abort_flag)) && ok;
-      tc_fence_after();
-      uint32_t s[128];
-      tmem_ld128(tmem + buf * 128 + lane_addr, s);
-      tc_fence_before();
-      mbar_arrive(bar(S::S_EMPTY + buf));
-      const float4* nl = reinterpret_cast<const float4*>(my_lse + lb * kTile);
+    int qi = 0;
+    for (int it = 0; ok; ++it) {
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(S::ITEM + it % kRing), (it / kRing) & 1, abort_flag));
+      const int4 e = items[it % kRing];
+      if (!ok || (e.y & kEnd)) break;
+      const int b = (int)((uint32_t)e.w >> 16), hk = e.w & 0xFFFF, key = e.z * kTile + r;
+      if (!(e.y & kEmpty)) {
+        if (qi % kGroups == wg) {
+          const int hg = e.y & 255, q0 = (e.x >> 1) * kTile, mine = qi / kGroups, lb = mine & 1;
+          const bool ragged = q0 + kTile > p.n_q, partial = (e.x & 1) || ragged;
+          // -LSE in log2 units of this thread's row of the query tile; -inf for rows that see no key and rows past n_q
+          // (their p is 0)
+          const float x = q0 + r < p.n_q ? __ldg(p.lse + ((int64_t)b * p.H + hk * p.q_per_kv + hg) * p.n_q + q0 + r) : kNegInf;
+          if (partial && at_head != (p.Hm == 1 ? 0 : hg)) {  // this key's bounds
+            const int64_t at = ((int64_t)b * p.Hm + (p.Hm == 1 ? 0 : hk * p.q_per_kv + hg)) * p.n_k + key;
+            const bool in = key < p.n_k;
+            lts = in && p.vec[0] ? __ldg(p.vec[0] + at) : p.n_q;
+            lte = in && p.vec[1] ? __ldg(p.vec[1] + at) : p.n_q;
+            uts = in && p.vec[2] ? __ldg(p.vec[2] + at) : 0;
+            ute = in && p.vec[3] ? __ldg(p.vec[3] + at) : 0;
+            at_head = p.Hm == 1 ? 0 : hg;
+          }
+          my_lse[lb * kTile + r] = x == kNegInf ? kNegInf : -x * 1.4426950408889634f;
+          if (x != x) misc_v[3] = 1;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(S::LSE_FULL + 2 * wg + lb));
+          // the values are there (and those of the item before last have been read)
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(S::LSE_FULL + 2 * wg + lb), (mine >> 1) & 1, abort_flag));
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(S::S_FULL + wg), mine & 1, abort_flag)) && ok;
+          if (!ok) break;
+          const bool numbers = misc_v[3] == 0;
+          const float* nl = my_lse + lb * kTile;
+          auto mask_word = [&](int jb) {  // bit i: query q0 + 32 jb + i does not see this key
+            const int base = q0 + jb * 32;
+            const uint32_t mw = interval_bits32(lts, lte, base) | interval_bits32(uts, ute, base);
+            return !ragged || base + 32 <= p.n_q ? mw : mw | (base >= p.n_q ? 0xFFFFFFFFu : 0xFFFFFFFFu << (p.n_q - base));
+          };
+          tc_fence_after();
 #pragma unroll
-      for (int c = 0; c < kTile; c += 4) {
-        const float4 v = nl[c / 4];
-        const uint64_t x0 = fma2(f2pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, f2pack(v.x, v.y));
-        const uint64_t x1 = fma2(f2pack(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), sc2, f2pack(v.z, v.w));
-        s[c] = __float_as_uint(ex2(f2lo(x0)));
-        s[c + 1] = __float_as_uint(ex2(f2hi(x0)));
-        s[c + 2] = __float_as_uint(ex2(f2lo(x1)));
-        s[c + 3] = __float_as_uint(ex2(f2hi(x1)));
-      }
-      if (partial) {
-#pragma unroll
-        for (int jb = 0; jb < 4; ++jb) {
-          const int base = q0 + jb * 32;
-          uint32_t mw = interval_bits32(lts, lte, base) | interval_bits32(uts, ute, base);
-          if (ragged) mw |= base + 32 <= p.n_q ? 0u : base >= p.n_q ? 0xFFFFFFFFu : 0xFFFFFFFFu << (p.n_q - base);
-          if (__any_sync(0xffffffffu, mw != 0u)) {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) s[jb * 32 + c] = ((mw >> c) & 1u) ? 0u : s[jb * 32 + c];
+          for (int jb = 0; jb < 4; ++jb) {
+            uint32_t s[32];
+            tmem_ld32(tmem + wg * 128 + jb * 32 + lane_addr, s);
+            if (jb == 3) {
+              tc_fence_before();
+              mbar_arrive(bar(S::S_EMPTY + wg));
+            }
+            const uint32_t masked = partial ? mask_word(jb) : 0u;
+            if (numbers) add_block<true>(s, nl + jb * 32, sc2, masked, acc);
+            else add_block<false>(s, nl + jb * 32, sc2, masked, acc);
           }
         }
+        ++qi;
       }
+      if (e.y & kLast) {  // the key tile is done: the other warpgroups' sums go to the first
+        const uint64_t a = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
+        sum = f2lo(a) + f2hi(a);
+        const int sb = ends & 1, turn = ends >> 1;
+        float* others = sum_s + sb * (kGroups - 1) * kTile;
+        if (wg > 0) {
+          if (turn > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(S::SUM_EMPTY + sb), (turn - 1) & 1, abort_flag));
+          others[(wg - 1) * kTile + r] = sum;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(S::SUM_FULL + sb));
+        } else {
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(S::SUM_FULL + sb), turn & 1, abort_flag));
 #pragma unroll
-      for (int c = 0; c < kTile; c += 8)
+          for (int g = 0; g < kGroups - 1; ++g) sum += others[g * kTile + r];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(S::SUM_EMPTY + sb));
+          key_at = key < p.n_k ? ((int64_t)b * p.H_kv + hk) * p.weight_stride + key : -1;
+          if (step == 1 && key_at >= 0) p.weight[key_at] = p.accumulate ? p.weight[key_at] + sum : sum;
+        }
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          acc[u] = add2(acc[u], f2pack(__uint_as_float(s[c + 2 * u]), __uint_as_float(s[c + 2 * u + 1])));
+        for (int u = 0; u < 4; ++u) acc[u] = 0;
+        ++ends;
+        at_head = -1;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(S::ITEM_FREE + it % kRing));
     }
     if (!ok && lane == 0) record_failure(p.status, abort_flag, 63);
-    const uint64_t a = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
-    sum = f2lo(a) + f2hi(a);
-    if (wg == 1) sum_s[r] = sum;
   }
 
   __syncthreads();  // (also: the MMA warp has drained)
-  if (warp < 4) {
-    sum += sum_s[threadIdx.x];
-    if (step > 1) sum_s[threadIdx.x] = sum;
-  }
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  if (step > 1) cluster_sync_all();
-  const int key = kt * kTile + (int)threadIdx.x;
-  if (rank == 0 && warp < 4 && key < p.n_k) {
-    for (int c = 1; c < step; ++c) sum += ld_cluster_f32(smem_u32(sum_s + threadIdx.x), c);
-    float* w = p.weight + ((int64_t)b * p.H_kv + hk) * p.weight_stride + key;
-    *w = p.accumulate ? *w + sum : sum;
+  if (step > 1) {  // one key tile per cluster
+    if (warp < 4) sum_s[threadIdx.x] = sum;
+    cluster_sync_all();
+    if (rank == 0 && warp < 4 && key_at >= 0) {
+      for (int c = 1; c < step; ++c) sum += ld_cluster_f32(smem_u32(sum_s + threadIdx.x), c);
+      p.weight[key_at] = p.accumulate ? p.weight[key_at] + sum : sum;
+    }
+    cluster_sync_all();  // no CTA leaves while its sums are read
   }
-  if (step > 1) cluster_sync_all();  // no CTA leaves while its sums are read
 }
 
 template <int D>
@@ -312,11 +458,10 @@ fm_status launch_key_weight(const fm_attn_args* a, const KeyWeightParams& p, int
     return FM_ERR_CUDA;
   if (!smem_opt_in<key_weight_kernel<D>>(S::kAlloc)) return FM_ERR_CUDA;
   // A key tile's query tiles are shared by a cluster of CTAs where there are too few key tiles for the SMs.
-  const int64_t tiles = (int64_t)p.T_k * H_kv * a->B;
   int cluster = 1;
-  while (cluster < 8 && tiles * cluster * 2 <= 148) cluster *= 2;
+  while (cluster < 8 && (int64_t)p.n_work * cluster * 2 <= kSMs) cluster *= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.T_k * cluster), H_kv, a->B);
+  cfg.gridDim = dim3((unsigned)(cluster > 1 ? p.n_work * cluster : p.n_work < kSMs ? p.n_work : kSMs));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = S::kAlloc;
   cfg.stream = stream;
@@ -343,6 +488,7 @@ extern "C" fm_status fm_attn_key_weight(const fm_attn_args* a, const fm_mask_met
   const fm_status st = fm::check_attn_args(&args, meta, vec);
   if (st != FM_OK) return st;
   if (args.dtype != 0) return FM_ERR_UNSUPPORTED;
+  if ((int64_t)args.B * args.H * ((args.n_k + 127) / 128) >= ((int64_t)1 << 31)) return FM_ERR_UNSUPPORTED;
   if (!lse || !weight || ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(weight)) & 3))
     return FM_ERR_INVALID_ARG;
   if (weight_stride < args.n_k || (accumulate != 0 && accumulate != 1)) return FM_ERR_INVALID_ARG;
@@ -365,6 +511,9 @@ extern "C" fm_status fm_attn_key_weight(const fm_attn_args* a, const fm_mask_met
   p.T_q = (args.n_q + fm::kTile - 1) / fm::kTile;
   p.T_k = (args.n_k + fm::kTile - 1) / fm::kTile;
   p.accumulate = accumulate;
+  p.n_bh = args.B * H_kv;
+  p.n_work = p.T_k * p.n_bh;
+  p.group = fm::dispatch_group(p.n_bh, 2.0 * args.n_q * args.D * p.q_per_kv);
   p.scale_log2 = args.scale * 1.4426950408889634f;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (args.D == 64) return fm::launch_key_weight<64>(&args, p, H_kv, s);
