@@ -27,7 +27,8 @@ constexpr int kListWarp = kGroups * 4, kMmaWarp = kListWarp + 1;
 constexpr int kSMs = 148;
 constexpr int kPolyEvery = 4;  // one score pair in kPolyEvery takes the polynomial instead of the MUFU unit
 constexpr int kBufs = kGroups;  // TMEM score buffers of 128 columns, one per warpgroup
-constexpr int kRing = 16;  // listed items
+constexpr int kRing = 8;      // listed items of a reader
+constexpr int kReaders = kGroups + 1;  // the warpgroups of sums, the MMA role
 constexpr float kNegInf = -__builtin_huge_valf();
 
 struct KeyWeightParams {
@@ -53,17 +54,19 @@ struct KeyWeightSmem {
   static constexpr int kQ = kK + kKBufs * kTileBytes;
   static constexpr int kLse = kQ + kStages * kTileBytes;     // [warpgroups][2][128] -log2 LSE
   static constexpr int kSum = kLse + kGroups * 2 * kTile * 4;  // [2][warpgroups - 1][128] sums; [0][0]: of the CTA
-  static constexpr int kItems = kSum + 2 * (kGroups - 1) * kTile * 4;  // int4 ring of the listed items
-  static constexpr int kBar = kItems + kRing * 16;
+  static constexpr int kItems = kSum + 2 * (kGroups - 1) * kTile * 4;  // int4 [readers][kRing]: listed items
+  static constexpr int kBar = kItems + kReaders * kRing * 16;
   enum { K_FULL, K_EMPTY = K_FULL + kKBufs, Q_FULL = K_EMPTY + kKBufs, Q_EMPTY = Q_FULL + kStages,
-         S_FULL = Q_EMPTY + kStages, S_EMPTY = S_FULL + kBufs, ITEM = S_EMPTY + kBufs, ITEM_FREE = ITEM + kRing,
-         LSE_FULL = ITEM_FREE + kRing, SUM_FULL = LSE_FULL + 2 * kGroups, SUM_EMPTY = SUM_FULL + 2, DRAIN = SUM_EMPTY + 2, kNumBars };
+         S_FULL = Q_EMPTY + kStages, S_EMPTY = S_FULL + kBufs, ITEM = S_EMPTY + kBufs, ITEM_FREE = ITEM + kReaders * kRing,
+         LSE_FULL = ITEM_FREE + kReaders * kRing, SUM_FULL = LSE_FULL + 2 * kGroups, SUM_EMPTY = SUM_FULL + 2, DRAIN = SUM_EMPTY + 2, kNumBars };
   static constexpr int kMisc = kBar + kNumBars * 8;  // [0] TMEM base, [1] abort flag, [2] zero, [3] an LSE was a NaN
   static constexpr int kBytes = kMisc + 16;
   static constexpr int kAlloc = kBytes + 1024;
 };
 // An item: .x query-tile entry (qt << 1 | partial), .y query head of the group and flags, .z key tile, .w b << 16 | hk.
-constexpr int kFirst = 1 << 8, kLast = 2 << 8, kEmpty = 4 << 8, kEnd = 8 << 8;  // of the key tile; no query tile; no item
+// Each reader has a ring of its own: the MMA role gets every query tile, with kFirst and kLast of its key tile; a
+// warpgroup of sums gets its query tiles, and after them a kLast item of the key tile without one.
+constexpr int kFirst = 1 << 8, kLast = 2 << 8, kEnd = 4 << 8;
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -132,8 +135,8 @@ __device__ __forceinline__ uint64_t exp2_poly5(uint64_t x2) {
   q2 = fma2(q2, f2, f2pack(kExp2W2, kExp2W2));
   q2 = fma2(q2, f2, f2pack(kExp2W1, kExp2W1));
   q2 = fma2(q2, f2, f2pack(kExp2W0, kExp2W0));
-  const uint32_t lo = (uint32_t)q2 + ((uint32_t)t2 << 23);
-  const uint32_t hi = (uint32_t)(q2 >> 32) + ((uint32_t)(t2 >> 32) << 23);
+  const uint32_t lo = (uint32_t)t2 * 0x800000u + (uint32_t)q2;  // (one multiply-add)
+  const uint32_t hi = (uint32_t)(t2 >> 32) * 0x800000u + (uint32_t)(q2 >> 32);
   return ((uint64_t)hi << 32) | lo;
 }
 
@@ -205,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kNumBars; ++i) mbar_init(bar(i), 1);
     for (int i = 0; i < kBufs; ++i) mbar_init(bar(S::S_EMPTY + i), kTile);
-    for (int i = 0; i < kRing; ++i) mbar_init(bar(S::ITEM_FREE + i), 4 * kGroups + 1);  // every warp of sums and the MMA role
+    for (int i = 0; i < kGroups * kRing; ++i) mbar_init(bar(S::ITEM_FREE + i), 4);  // a warpgroup's warps
     for (int i = 0; i < 2 * kGroups; ++i) mbar_init(bar(S::LSE_FULL + i), 4);  // a warpgroup's warps
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(S::SUM_FULL + i), 4 * (kGroups - 1));
@@ -231,22 +234,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kListWarp) {
     // ------------------------------------------------------- list and load role
     if (lane == 0) {
-      int it = 0, qi = 0, wk = 0;  // items, query tiles and key tiles so far
+      int qi = 0, wk = 0;  // query tiles and key tiles so far
+      int pushed[kReaders];
+#pragma unroll
+      for (int i = 0; i < kReaders; ++i) pushed[i] = 0;
       bool ok = true;
-      auto push = [&](int entry, int hg_flags, int kt, int b_hk) {
-        if (it >= kRing && !mbar_wait(bar(S::ITEM_FREE + it % kRing), (it / kRing - 1) & 1, abort_flag)) {
+      auto push = [&](int reader, int& n, const int4& e) {
+        const int at = reader * kRing + n % kRing;
+        if (n >= kRing && !mbar_wait(bar(S::ITEM_FREE + at), (n / kRing - 1) & 1, abort_flag)) {
           ok = false;
           return;
         }
-        items[it % kRing] = make_int4(entry, hg_flags, kt, b_hk);
-        mbar_arrive(bar(S::ITEM + it % kRing));
-        ++it;
+        items[at] = e;
+        mbar_arrive(bar(S::ITEM + at));
+        ++n;
       };
       int bh = 0, kt = 0;
       if (work0 < p.n_work) work_of(p, work0, bh, kt);
-      for (int w = work0; ok && w < p.n_work; w += work_step) {
+      // rounds of one key tile per CTA, every other one in reverse: the first of a round has its longest list
+      for (int round = 0, w = work0; ok && w < p.n_work; ++round) {
         int bh_next = 0, kt_next = 0;
-        if (w + work_step < p.n_work) work_of(p, w + work_step, bh_next, kt_next);  // (in flight until it is used)
+        const int w_next = (round + 1) * work_step + ((round & 1) ? work0 : work_step - 1 - work0);
+        if (w_next < p.n_work) work_of(p, w_next, bh_next, kt_next);  // (in flight until it is used)
         const int b = bh / p.H_kv, hk = bh % p.H_kv;
         const int b_hk = (int)((uint32_t)b << 16 | (uint32_t)hk);
         const int64_t bhm0 = (int64_t)b * p.Hm + (p.Hm == 1 ? 0 : hk * p.q_per_kv);
@@ -259,7 +268,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         walk.start(rank);
         int hg, entry;
         bool more = walk.get(hg, entry);
-        if (!more) push(0, kEmpty | kLast, kt, b_hk);
         for (bool first = true; ok && more; first = false) {
           const int cur_hg = hg, cur = entry;
           walk.at += step;
@@ -284,13 +292,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < kAtoms; ++c)
             tma_load_4d(q_s + st * S::kTileBytes + c * 16384, &tm_q, bar(S::Q_FULL + st), c * 64,
                         hk * p.q_per_kv + cur_hg, (cur >> 1) * kTile, b);
+          const int4 e = make_int4(cur, cur_hg | (first ? kFirst : 0) | (more ? 0 : kLast), kt, b_hk);
+          push(kGroups, pushed[kGroups], e);
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g)
+            if (qi % kGroups == g) push(g, pushed[g], make_int4(cur, cur_hg, kt, b_hk));
           ++qi;
-          push(cur, cur_hg | (first ? kFirst : 0) | (more ? 0 : kLast), kt, b_hk);
         }
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) push(g, pushed[g], make_int4(0, kLast, kt, b_hk));
         bh = bh_next;
         kt = kt_next;
+        w = w_next;
       }
-      if (ok) push(0, kEnd, 0, 0);
+#pragma unroll
+      for (int i = 0; i < kReaders; ++i) push(i, pushed[i], make_int4(0, kEnd, 0, 0));
       if (!ok) record_failure(p.status, abort_flag, 61);
       // the copies in flight land before this role ends (a consumer that gave up may leave some unread)
       for (int x = max(wk - S::kKBufs, 0); x < wk; ++x) mbar_wait(bar(S::K_FULL + x % S::kKBufs), (x / S::kKBufs) & 1, never);
@@ -305,14 +321,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int qi = 0, wk = 0;
       for (int it = 0;; ++it) {
-        if (!mbar_wait(bar(S::ITEM + it % kRing), (it / kRing) & 1, abort_flag)) {
+        const int slot = kGroups * kRing + it % kRing;
+        if (!mbar_wait(bar(S::ITEM + slot), (it / kRing) & 1, abort_flag)) {
           ok = false;
           break;
         }
-        const int flags = items[it % kRing].y;
-        mbar_arrive(bar(S::ITEM_FREE + it % kRing));
+        const int flags = items[slot].y;
+        mbar_arrive(bar(S::ITEM_FREE + slot));
         if (flags & kEnd) break;
-        if (flags & kEmpty) continue;
         const int st = qi % S::kStages, buf = qi % kBufs, kb = wk % S::kKBufs;
         if (((flags & kFirst) && !mbar_wait(bar(S::K_FULL + kb), (wk / S::kKBufs) & 1, abort_flag)) ||
             !mbar_wait(bar(S::Q_FULL + st), (qi / S::kStages) & 1, abort_flag) ||
@@ -349,60 +365,60 @@ __global__ void __launch_bounds__(kThreads, 1)
     int at_head = -1, ends = 0;
     int32_t lts = 0, lte = 0, uts = 0, ute = 0;
     bool ok = true;
-    int qi = 0;
+    int mine = 0;  // query tiles so far
     for (int it = 0; ok; ++it) {
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(S::ITEM + it % kRing), (it / kRing) & 1, abort_flag));
-      const int4 e = items[it % kRing];
+      const int slot = wg * kRing + it % kRing;
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(S::ITEM + slot), (it / kRing) & 1, abort_flag));
+      const int4 e = items[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(S::ITEM_FREE + slot));
       if (!ok || (e.y & kEnd)) break;
       const int b = (int)((uint32_t)e.w >> 16), hk = e.w & 0xFFFF, key = e.z * kTile + r;
-      if (!(e.y & kEmpty)) {
-        if (qi % kGroups == wg) {
-          const int hg = e.y & 255, q0 = (e.x >> 1) * kTile, mine = qi / kGroups, lb = mine & 1;
-          const bool ragged = q0 + kTile > p.n_q, partial = (e.x & 1) || ragged;
-          // -LSE in log2 units of this thread's row of the query tile; -inf for rows that see no key and rows past n_q
-          // (their p is 0)
-          const float x = q0 + r < p.n_q ? __ldg(p.lse + ((int64_t)b * p.H + hk * p.q_per_kv + hg) * p.n_q + q0 + r) : kNegInf;
-          if (partial && at_head != (p.Hm == 1 ? 0 : hg)) {  // this key's bounds
-            const int64_t at = ((int64_t)b * p.Hm + (p.Hm == 1 ? 0 : hk * p.q_per_kv + hg)) * p.n_k + key;
-            const bool in = key < p.n_k;
-            lts = in && p.vec[0] ? __ldg(p.vec[0] + at) : p.n_q;
-            lte = in && p.vec[1] ? __ldg(p.vec[1] + at) : p.n_q;
-            uts = in && p.vec[2] ? __ldg(p.vec[2] + at) : 0;
-            ute = in && p.vec[3] ? __ldg(p.vec[3] + at) : 0;
-            at_head = p.Hm == 1 ? 0 : hg;
-          }
-          my_lse[lb * kTile + r] = x == kNegInf ? kNegInf : -x * 1.4426950408889634f;
-          if (x != x) misc_v[3] = 1;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(S::LSE_FULL + 2 * wg + lb));
-          // the values are there (and those of the item before last have been read)
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(S::LSE_FULL + 2 * wg + lb), (mine >> 1) & 1, abort_flag));
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(S::S_FULL + wg), mine & 1, abort_flag)) && ok;
-          if (!ok) break;
-          const bool numbers = misc_v[3] == 0;
-          const float* nl = my_lse + lb * kTile;
-          auto mask_word = [&](int jb) {  // bit i: query q0 + 32 jb + i does not see this key
-            const int base = q0 + jb * 32;
-            const uint32_t mw = interval_bits32(lts, lte, base) | interval_bits32(uts, ute, base);
-            return !ragged || base + 32 <= p.n_q ? mw : mw | (base >= p.n_q ? 0xFFFFFFFFu : 0xFFFFFFFFu << (p.n_q - base));
-          };
-          tc_fence_after();
-#pragma unroll
-          for (int jb = 0; jb < 4; ++jb) {
-            uint32_t s[32];
-            tmem_ld32(tmem + wg * 128 + jb * 32 + lane_addr, s);
-            if (jb == 3) {
-              tc_fence_before();
-              mbar_arrive(bar(S::S_EMPTY + wg));
-            }
-            const uint32_t masked = partial ? mask_word(jb) : 0u;
-            if (numbers) add_block<true>(s, nl + jb * 32, sc2, masked, acc);
-            else add_block<false>(s, nl + jb * 32, sc2, masked, acc);
-          }
+      if (!(e.y & kLast)) {
+        const int hg = e.y & 255, q0 = (e.x >> 1) * kTile, lb = mine & 1;
+        const bool ragged = q0 + kTile > p.n_q, partial = (e.x & 1) || ragged;
+        // -LSE in log2 units of this thread's row of the query tile; -inf for rows that see no key and rows past n_q
+        // (their p is 0)
+        const float x = q0 + r < p.n_q ? __ldg(p.lse + ((int64_t)b * p.H + hk * p.q_per_kv + hg) * p.n_q + q0 + r) : kNegInf;
+        if (partial && at_head != (p.Hm == 1 ? 0 : hg)) {  // this key's bounds
+          const int64_t at = ((int64_t)b * p.Hm + (p.Hm == 1 ? 0 : hk * p.q_per_kv + hg)) * p.n_k + key;
+          const bool in = key < p.n_k;
+          lts = in && p.vec[0] ? __ldg(p.vec[0] + at) : p.n_q;
+          lte = in && p.vec[1] ? __ldg(p.vec[1] + at) : p.n_q;
+          uts = in && p.vec[2] ? __ldg(p.vec[2] + at) : 0;
+          ute = in && p.vec[3] ? __ldg(p.vec[3] + at) : 0;
+          at_head = p.Hm == 1 ? 0 : hg;
         }
-        ++qi;
-      }
-      if (e.y & kLast) {  // the key tile is done: the other warpgroups' sums go to the first
+        my_lse[lb * kTile + r] = x == kNegInf ? kNegInf : -x * 1.4426950408889634f;
+        if (x != x) misc_v[3] = 1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(S::LSE_FULL + 2 * wg + lb));
+        // the values are there (and those of the item before last have been read)
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(S::LSE_FULL + 2 * wg + lb), (mine >> 1) & 1, abort_flag));
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(S::S_FULL + wg), mine & 1, abort_flag)) && ok;
+        if (!ok) break;
+        const bool numbers = misc_v[3] == 0;
+        const float* nl = my_lse + lb * kTile;
+        auto mask_word = [&](int jb) {  // bit i: query q0 + 32 jb + i does not see this key
+          const int base = q0 + jb * 32;
+          const uint32_t mw = interval_bits32(lts, lte, base) | interval_bits32(uts, ute, base);
+          return !ragged || base + 32 <= p.n_q ? mw : mw | (base >= p.n_q ? 0xFFFFFFFFu : 0xFFFFFFFFu << (p.n_q - base));
+        };
+        tc_fence_after();
+#pragma unroll 1  // (the code of one block stays in the instruction cache)
+        for (int jb = 0; jb < 4; ++jb) {
+          uint32_t s[32];
+          tmem_ld32(tmem + wg * 128 + jb * 32 + lane_addr, s);
+          if (jb == 3) {
+            tc_fence_before();
+            mbar_arrive(bar(S::S_EMPTY + wg));
+          }
+          const uint32_t masked = partial ? mask_word(jb) : 0u;
+          if (numbers) add_block<true>(s, nl + jb * 32, sc2, masked, acc);
+          else add_block<false>(s, nl + jb * 32, sc2, masked, acc);
+        }
+        ++mine;
+      } else {  // the key tile is done: the other warpgroups' sums go to the first
         const uint64_t a = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
         sum = f2lo(a) + f2hi(a);
         const int sb = ends & 1, turn = ends >> 1;
@@ -426,8 +442,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++ends;
         at_head = -1;
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(S::ITEM_FREE + it % kRing));
     }
     if (!ok && lane == 0) record_failure(p.status, abort_flag, 63);
   }
