@@ -9,8 +9,8 @@
 // bits per 32 queries.  One CTA per SM works through a fixed share of the key tiles, longest lists first, and the
 // copies and products of the next key tile start while the last one is still being summed.  Where there are too few
 // key tiles for the SMs a cluster of CTAs shares each one's query tiles and adds up through distributed shared memory.
-// Per score there is one exponential against 2 D flops of the tensor core: for D = 128 the MUFU unit alone would take
-// 1024 clocks for a tile's 16384 (16 a clock) against 512 of the product, so a part of them goes to the FMA pipe.
+// Per score there is one exponential against 2 D flops of the tensor core: for D = 128 the MUFU unit takes 1024 clocks for
+// a tile's 16384 (16 a clock) against 512 of the product.
 // Four warpgroups take the query tiles in turn (so that one's waits hide behind the others' exponentials), one warp lists
 // the items and issues the TMA loads, one issues the MMAs.
 #include "fm_common.cuh"
@@ -25,7 +25,6 @@ constexpr int kGroups = 4;    // warpgroups of sums
 constexpr int kThreads = kGroups * 128 + 64;
 constexpr int kListWarp = kGroups * 4, kMmaWarp = kListWarp + 1;
 constexpr int kSMs = 148;
-constexpr int kPolyEvery = 4;  // one score pair in kPolyEvery takes the polynomial instead of the MUFU unit
 constexpr int kBufs = kGroups;  // TMEM score buffers of 128 columns, one per warpgroup
 constexpr int kRing = 8;      // listed items of a reader
 constexpr int kReaders = kGroups + 1;  // the warpgroups of sums, the MMA role
@@ -59,14 +58,40 @@ struct KeyWeightSmem {
   enum { K_FULL, K_EMPTY = K_FULL + kKBufs, Q_FULL = K_EMPTY + kKBufs, Q_EMPTY = Q_FULL + kStages,
          S_FULL = Q_EMPTY + kStages, S_EMPTY = S_FULL + kBufs, ITEM = S_EMPTY + kBufs, ITEM_FREE = ITEM + kReaders * kRing,
          LSE_FULL = ITEM_FREE + kReaders * kRing, SUM_FULL = LSE_FULL + 2 * kGroups, SUM_EMPTY = SUM_FULL + 2, DRAIN = SUM_EMPTY + 2, kNumBars };
-  static constexpr int kMisc = kBar + kNumBars * 8;  // [0] TMEM base, [1] abort flag, [2] zero, [3] an LSE was a NaN
+  static constexpr int kMisc = kBar + kNumBars * 8;  // [0] TMEM base, [1] abort flag, [2] zero
   static constexpr int kBytes = kMisc + 16;
   static constexpr int kAlloc = kBytes + 1024;
 };
 // An item: .x query-tile entry (qt << 1 | partial), .y query head of the group and flags, .z key tile, .w b << 16 | hk.
 // Each reader has a ring of its own: the MMA role gets every query tile, with kFirst and kLast of its key tile; a
-// warpgroup of sums gets its query tiles, and after them a kLast item of the key tile without one.
-constexpr int kFirst = 1 << 8, kLast = 2 << 8, kEnd = 4 << 8;
+// warpgroup of sums gets its query tiles, with kLast at its last one of the key tile, or a kLast | kEmpty item if it has none.
+constexpr int kFirst = 1 << 8, kLast = 2 << 8, kEmpty = 4 << 8, kEnd = 8 << 8;
+
+// Has the phase of the given parity completed?  (Never waits, as try_wait may.)
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// mbar_wait for the two roles of one thread, which are usually ahead: their polling takes no issue slots from the sums.
+__device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity, const volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  for (uint32_t it = 1;; ++it) {
+    __nanosleep(32);
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 63u) == 0) {
+      if (*abort) return false;
+      if (globaltimer() - t0 > kTimeoutNs) return false;
+    }
+  }
+}
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -120,56 +145,39 @@ struct ItemWalk {
   }
 };
 
-// 2^x for a pair on the FMA and integer pipes, as exp2_poly2 but with the degree-5 minimax polynomial (relative error
-// 2.4e-7, a fourth of the MUFU unit's ulps more): the weights are fp32 results.  x <= 127; below -125 it gives 2^-125.
-constexpr float kExp2W0 = 1.000000119e+00f, kExp2W1 = 6.931469440e-01f, kExp2W2 = 2.402212024e-01f,
-                kExp2W3 = 5.550713092e-02f, kExp2W4 = 9.675540961e-03f, kExp2W5 = 1.327647245e-03f;
-__device__ __forceinline__ uint64_t exp2_poly5(uint64_t x2) {
-  constexpr float kRound = 12582912.0f;  // 1.5 * 2^23
-  const uint64_t xc = f2pack(fmaxf(f2lo(x2), -125.f), fmaxf(f2hi(x2), -125.f));
-  const uint64_t t2 = add2(xc, f2pack(kRound, kRound));
-  const uint64_t r2 = add2(t2, f2pack(-kRound, -kRound));
-  const uint64_t f2 = fma2(r2, f2pack(-1.f, -1.f), xc);
-  uint64_t q2 = fma2(f2, f2pack(kExp2W5, kExp2W5), f2pack(kExp2W4, kExp2W4));
-  q2 = fma2(q2, f2, f2pack(kExp2W3, kExp2W3));
-  q2 = fma2(q2, f2, f2pack(kExp2W2, kExp2W2));
-  q2 = fma2(q2, f2, f2pack(kExp2W1, kExp2W1));
-  q2 = fma2(q2, f2, f2pack(kExp2W0, kExp2W0));
-  const uint32_t lo = (uint32_t)t2 * 0x800000u + (uint32_t)q2;  // (one multiply-add)
-  const uint32_t hi = (uint32_t)(t2 >> 32) * 0x800000u + (uint32_t)(q2 >> 32);
-  return ((uint64_t)hi << 32) | lo;
+// 16 columns of this thread's TMEM lane: the load, and the wait for every load so far (which the registers are tied to, so
+// that none of them is read before it).
+__device__ __forceinline__ void tmem_ld16_start(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16_end(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
 
-// Adds the weights of 32 scores to the four running pairs; bit i of `masked`: query i does not see the key.  nl: -LSE of the
-// queries in log2 units.  kPoly: one pair in kPolyEvery goes to the FMA pipe (not once a row's LSE was a NaN, which the
-// polynomial would not pass on).
-template <bool kPoly>
-__device__ __forceinline__ void add_block(uint32_t (&s)[32], const float* nl, uint64_t sc2, uint32_t masked, uint64_t (&acc)[4]) {
+// Adds the weights of 16 scores to the four running sums; bit i of `masked`: query i does not see the key.  nl: -LSE of the
+// queries in log2 units.  (One score an instruction: packed pairs would halve the multiply-adds and additions, but cost
+// more register moves than that.)
+__device__ __forceinline__ void add_block(const uint32_t (&s)[16], const float* nl, float scale, uint32_t masked, float (&acc)[4]) {
+  float w[16];
 #pragma unroll
-  for (int c = 0; c < 32; c += 4) {
+  for (int c = 0; c < 16; c += 4) {
     const float4 v = *reinterpret_cast<const float4*>(nl + c);
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int i = c + 2 * u;
-      const uint64_t x = fma2(f2pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), sc2, u ? f2pack(v.z, v.w) : f2pack(v.x, v.y));
-      if (kPoly && (i / 2) % kPolyEvery == 0) {
-        const uint64_t y = exp2_poly5(x);
-        s[i] = (uint32_t)y;
-        s[i + 1] = (uint32_t)(y >> 32);
-      } else {
-        s[i] = __float_as_uint(ex2(f2lo(x)));
-        s[i + 1] = __float_as_uint(ex2(f2hi(x)));
-      }
-    }
+    w[c] = ex2(fmaf(__uint_as_float(s[c]), scale, v.x));
+    w[c + 1] = ex2(fmaf(__uint_as_float(s[c + 1]), scale, v.y));
+    w[c + 2] = ex2(fmaf(__uint_as_float(s[c + 2]), scale, v.z));
+    w[c + 3] = ex2(fmaf(__uint_as_float(s[c + 3]), scale, v.w));
   }
   if (__any_sync(0xffffffffu, masked != 0u)) {
 #pragma unroll
-    for (int c = 0; c < 32; ++c) s[c] = ((masked >> c) & 1u) ? 0u : s[c];
+    for (int c = 0; c < 16; ++c) w[c] = ((masked >> c) & 1u) ? 0.f : w[c];
   }
 #pragma unroll
-  for (int c = 0; c < 32; c += 8)
-#pragma unroll
-    for (int u = 0; u < 4; ++u) acc[u] = add2(acc[u], f2pack(__uint_as_float(s[c + 2 * u]), __uint_as_float(s[c + 2 * u + 1])));
+  for (int c = 0; c < 16; ++c) acc[c & 3] += w[c];
 }
 
 // The key tile and head of piece of work `w`: groups of heads, in each the key tiles by rank (longest lists first).
@@ -199,7 +207,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + S::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
   const volatile int* never = reinterpret_cast<const volatile int*>(misc + 2);
-  volatile uint32_t* misc_v = misc;
   const uint32_t k_s = smem_u32(smem + S::kK), q_s = smem_u32(smem + S::kQ);
   float* lse_s = reinterpret_cast<float*>(smem + S::kLse);
   float* sum_s = reinterpret_cast<float*>(smem + S::kSum);
@@ -215,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(S::SUM_EMPTY + i), 4);
     }
     *abort_flag = 0;
-    misc[2] = misc[3] = 0;
+    misc[2] = 0;
     fence_barrier_init();
     prefetch_tmap(&tm_q);
     prefetch_tmap(&tm_k);
@@ -241,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       auto push = [&](int reader, int& n, const int4& e) {
         const int at = reader * kRing + n % kRing;
-        if (n >= kRing && !mbar_wait(bar(S::ITEM_FREE + at), (n / kRing - 1) & 1, abort_flag)) {
+        if (n >= kRing && !mbar_wait_idle(bar(S::ITEM_FREE + at), (n / kRing - 1) & 1, abort_flag)) {
           ok = false;
           return;
         }
@@ -265,16 +272,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         walk.head_count = p.Hm == 1 ? 0 : p.T_k;
         walk.head_entries = p.Hm == 1 ? 0 : (int64_t)p.T_k * p.T_q;
         walk.heads = p.q_per_kv;
+        // query tiles of this key tile that this CTA takes
+        int total = 0;
+        if (p.Hm == 1) total = __ldg(walk.count) * p.q_per_kv;
+        else
+          for (int h = 0; h < p.q_per_kv; ++h) total += __ldg(walk.count + h * walk.head_count);
+        const int n_items = total > rank ? (total - rank + step - 1) / step : 0;
         walk.start(rank);
-        int hg, entry;
+        int hg, entry, at = 0;
         bool more = walk.get(hg, entry);
-        for (bool first = true; ok && more; first = false) {
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
+          if ((g - qi % kGroups + kGroups) % kGroups >= n_items) push(g, pushed[g], make_int4(0, kLast | kEmpty, kt, b_hk));
+        for (bool first = true; ok && more; first = false, ++at) {
           const int cur_hg = hg, cur = entry;
           walk.at += step;
           more = walk.get(hg, entry);  // (the next entry, in flight during this one's copies)
           if (first) {
             const int kb = wk % S::kKBufs;
-            if (wk >= S::kKBufs && !mbar_wait(bar(S::K_EMPTY + kb), (wk / S::kKBufs - 1) & 1, abort_flag)) {
+            if (wk >= S::kKBufs && !mbar_wait_idle(bar(S::K_EMPTY + kb), (wk / S::kKBufs - 1) & 1, abort_flag)) {
               ok = false;
               break;
             }
@@ -284,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++wk;
           }
           const int st = qi % S::kStages;
-          if (qi >= S::kStages && !mbar_wait(bar(S::Q_EMPTY + st), (qi / S::kStages - 1) & 1, abort_flag)) {
+          if (qi >= S::kStages && !mbar_wait_idle(bar(S::Q_EMPTY + st), (qi / S::kStages - 1) & 1, abort_flag)) {
             ok = false;
             break;
           }
@@ -296,11 +312,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           push(kGroups, pushed[kGroups], e);
 #pragma unroll
           for (int g = 0; g < kGroups; ++g)
-            if (qi % kGroups == g) push(g, pushed[g], make_int4(cur, cur_hg, kt, b_hk));
+            if (qi % kGroups == g) push(g, pushed[g], make_int4(cur, cur_hg | (at + kGroups >= n_items ? kLast : 0), kt, b_hk));
           ++qi;
         }
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) push(g, pushed[g], make_int4(0, kLast, kt, b_hk));
         bh = bh_next;
         kt = kt_next;
         w = w_next;
@@ -322,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int qi = 0, wk = 0;
       for (int it = 0;; ++it) {
         const int slot = kGroups * kRing + it % kRing;
-        if (!mbar_wait(bar(S::ITEM + slot), (it / kRing) & 1, abort_flag)) {
+        if (!mbar_wait_idle(bar(S::ITEM + slot), (it / kRing) & 1, abort_flag)) {
           ok = false;
           break;
         }
@@ -330,9 +344,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(bar(S::ITEM_FREE + slot));
         if (flags & kEnd) break;
         const int st = qi % S::kStages, buf = qi % kBufs, kb = wk % S::kKBufs;
-        if (((flags & kFirst) && !mbar_wait(bar(S::K_FULL + kb), (wk / S::kKBufs) & 1, abort_flag)) ||
-            !mbar_wait(bar(S::Q_FULL + st), (qi / S::kStages) & 1, abort_flag) ||
-            (qi >= kBufs && !mbar_wait(bar(S::S_EMPTY + buf), (qi / kBufs - 1) & 1, abort_flag))) {
+        if (((flags & kFirst) && !mbar_wait_idle(bar(S::K_FULL + kb), (wk / S::kKBufs) & 1, abort_flag)) ||
+            !mbar_wait_idle(bar(S::Q_FULL + st), (qi / S::kStages) & 1, abort_flag) ||
+            (qi >= kBufs && !mbar_wait_idle(bar(S::S_EMPTY + buf), (qi / kBufs - 1) & 1, abort_flag))) {
           ok = false;
           break;
         }
@@ -360,67 +374,103 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int wg = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
     float* my_lse = lse_s + wg * 2 * kTile;
-    const uint64_t sc2 = f2pack(p.scale_log2, p.scale_log2);
-    uint64_t acc[4] = {0, 0, 0, 0};
-    int at_head = -1, ends = 0;
-    int32_t lts = 0, lte = 0, uts = 0, ute = 0;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    int ends = 0;
     bool ok = true;
     int mine = 0;  // query tiles so far
+    // LSE of this thread's row of an item's query tile; -inf past n_q (and for rows that see no key): their p is 0
+    auto load_lse = [&](const int4& e) {
+      const int row = (e.x >> 1) * kTile + r, h = (e.w & 0xFFFF) * p.q_per_kv + (e.y & 255);
+      return row < p.n_q && !(e.y & (kEmpty | kEnd)) ? __ldg(p.lse + ((int64_t)((uint32_t)e.w >> 16) * p.H + h) * p.n_q + row) : kNegInf;
+    };
+    // bounds of this thread's key for an item: lts, lte, uts, ute
+    auto load_bounds = [&](const int4& e) {
+      const int b = (int)((uint32_t)e.w >> 16), key = e.z * kTile + r;
+      const int hm = p.Hm == 1 ? 0 : (e.w & 0xFFFF) * p.q_per_kv + (e.y & 255);
+      const int64_t at = ((int64_t)b * p.Hm + hm) * p.n_k + key;
+      const bool in = key < p.n_k && !(e.y & (kEmpty | kEnd));
+      int4 v;
+      v.x = in && p.vec[0] ? __ldg(p.vec[0] + at) : p.n_q;
+      v.y = in && p.vec[1] ? __ldg(p.vec[1] + at) : p.n_q;
+      v.z = in && p.vec[2] ? __ldg(p.vec[2] + at) : 0;
+      v.w = in && p.vec[3] ? __ldg(p.vec[3] + at) : 0;
+      return v;
+    };
+    int4 e_next, bounds_next;
+    float x_next = 0.f;
+    bool have_next = false;
     for (int it = 0; ok; ++it) {
-      const int slot = wg * kRing + it % kRing;
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(S::ITEM + slot), (it / kRing) & 1, abort_flag));
-      const int4 e = items[slot];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(S::ITEM_FREE + slot));
-      if (!ok || (e.y & kEnd)) break;
-      const int b = (int)((uint32_t)e.w >> 16), hk = e.w & 0xFFFF, key = e.z * kTile + r;
-      if (!(e.y & kLast)) {
-        const int hg = e.y & 255, q0 = (e.x >> 1) * kTile, lb = mine & 1;
-        const bool ragged = q0 + kTile > p.n_q, partial = (e.x & 1) || ragged;
-        // -LSE in log2 units of this thread's row of the query tile; -inf for rows that see no key and rows past n_q
-        // (their p is 0)
-        const float x = q0 + r < p.n_q ? __ldg(p.lse + ((int64_t)b * p.H + hk * p.q_per_kv + hg) * p.n_q + q0 + r) : kNegInf;
-        if (partial && at_head != (p.Hm == 1 ? 0 : hg)) {  // this key's bounds
-          const int64_t at = ((int64_t)b * p.Hm + (p.Hm == 1 ? 0 : hk * p.q_per_kv + hg)) * p.n_k + key;
-          const bool in = key < p.n_k;
-          lts = in && p.vec[0] ? __ldg(p.vec[0] + at) : p.n_q;
-          lte = in && p.vec[1] ? __ldg(p.vec[1] + at) : p.n_q;
-          uts = in && p.vec[2] ? __ldg(p.vec[2] + at) : 0;
-          ute = in && p.vec[3] ? __ldg(p.vec[3] + at) : 0;
-          at_head = p.Hm == 1 ? 0 : hg;
-        }
+      auto take = [&](int i) {  // reads a listed item and gives its place back
+        const int slot = wg * kRing + i % kRing;
+        const int4 v = items[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(S::ITEM_FREE + slot));
+        return v;
+      };
+      int4 e, bounds;
+      float x;
+      if (have_next) {
+        e = e_next;
+        x = x_next;
+        bounds = bounds_next;
+      } else {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(S::ITEM + wg * kRing + it % kRing), (it / kRing) & 1, abort_flag));
+        if (!ok) break;
+        e = take(it);
+        x = load_lse(e);
+        bounds = load_bounds(e);
+      }
+      if (e.y & kEnd) break;
+      const int b = (int)((uint32_t)e.w >> 16), hk = e.w & 0xFFFF, key = e.z * kTile + r, lb = mine & 1;
+      if (!(e.y & kEmpty)) {
         my_lse[lb * kTile + r] = x == kNegInf ? kNegInf : -x * 1.4426950408889634f;
-        if (x != x) misc_v[3] = 1;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(S::LSE_FULL + 2 * wg + lb));
+      }
+      // the next item, if it is listed already: its LSE and bounds are in flight during this one's exponentials
+      have_next = __all_sync(0xffffffffu, mbar_test(bar(S::ITEM + wg * kRing + (it + 1) % kRing), ((it + 1) / kRing) & 1));
+      if (have_next) {
+        e_next = take(it + 1);
+        x_next = load_lse(e_next);
+        bounds_next = load_bounds(e_next);
+      }
+      if (!(e.y & kEmpty)) {
+        const int q0 = (e.x >> 1) * kTile;
+        const bool ragged = q0 + kTile > p.n_q, partial = (e.x & 1) || ragged;
         // the values are there (and those of the item before last have been read)
         ok = __all_sync(0xffffffffu, mbar_wait(bar(S::LSE_FULL + 2 * wg + lb), (mine >> 1) & 1, abort_flag));
         ok = __all_sync(0xffffffffu, mbar_wait(bar(S::S_FULL + wg), mine & 1, abort_flag)) && ok;
         if (!ok) break;
-        const bool numbers = misc_v[3] == 0;
         const float* nl = my_lse + lb * kTile;
         auto mask_word = [&](int jb) {  // bit i: query q0 + 32 jb + i does not see this key
           const int base = q0 + jb * 32;
-          const uint32_t mw = interval_bits32(lts, lte, base) | interval_bits32(uts, ute, base);
+          const uint32_t mw = interval_bits32(bounds.x, bounds.y, base) | interval_bits32(bounds.z, bounds.w, base);
           return !ragged || base + 32 <= p.n_q ? mw : mw | (base >= p.n_q ? 0xFFFFFFFFu : 0xFFFFFFFFu << (p.n_q - base));
         };
         tc_fence_after();
-#pragma unroll 1  // (the code of one block stays in the instruction cache)
+        // 16 scores at a time, the next 16 in flight
+        uint32_t s0[16], s1[16];
+        const uint32_t t0 = tmem + wg * 128 + lane_addr;
+        tmem_ld16_start(t0, s0);
+#pragma unroll 1  // (the code of two blocks stays in the instruction cache)
         for (int jb = 0; jb < 4; ++jb) {
-          uint32_t s[32];
-          tmem_ld32(tmem + wg * 128 + jb * 32 + lane_addr, s);
-          if (jb == 3) {
+          const uint32_t masked = partial ? mask_word(jb) : 0u;
+          tmem_ld16_end(s0);
+          tmem_ld16_start(t0 + jb * 32 + 16, s1);
+          add_block(s0, nl + jb * 32, p.scale_log2, masked & 0xFFFFu, acc);
+          tmem_ld16_end(s1);
+          if (jb < 3) {
+            tmem_ld16_start(t0 + jb * 32 + 32, s0);
+          } else {
             tc_fence_before();
             mbar_arrive(bar(S::S_EMPTY + wg));
           }
-          const uint32_t masked = partial ? mask_word(jb) : 0u;
-          if (numbers) add_block<true>(s, nl + jb * 32, sc2, masked, acc);
-          else add_block<false>(s, nl + jb * 32, sc2, masked, acc);
+          add_block(s1, nl + jb * 32 + 16, p.scale_log2, masked >> 16, acc);
         }
         ++mine;
-      } else {  // the key tile is done: the other warpgroups' sums go to the first
-        const uint64_t a = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
-        sum = f2lo(a) + f2hi(a);
+      }
+      if (e.y & kLast) {  // the key tile is done: the other warpgroups' sums go to the first
+        sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
         const int sb = ends & 1, turn = ends >> 1;
         float* others = sum_s + sb * (kGroups - 1) * kTile;
         if (wg > 0) {
@@ -438,9 +488,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (step == 1 && key_at >= 0) p.weight[key_at] = p.accumulate ? p.weight[key_at] + sum : sum;
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) acc[u] = 0;
+        for (int u = 0; u < 4; ++u) acc[u] = 0.f;
         ++ends;
-        at_head = -1;
       }
     }
     if (!ok && lane == 0) record_failure(p.status, abort_flag, 63);
