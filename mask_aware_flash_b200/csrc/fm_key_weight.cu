@@ -11,8 +11,8 @@
 // key tiles for the SMs a cluster of CTAs shares each one's query tiles and adds up through distributed shared memory.
 // Per score there is one exponential against 2 D flops of the tensor core: for D = 128 the MUFU unit takes 1024 clocks for
 // a tile's 16384 (16 a clock) against 512 of the product.
-// Four warpgroups take the query tiles in turn (so that one's waits hide behind the others' exponentials), one warp lists
-// the items and issues the TMA loads, one issues the MMAs.
+// Four warpgroups take the query tiles in turn (so that one's waits hide behind the others' exponentials); one warp lists
+// the items for everybody, some key tiles ahead, one issues the TMA loads, one the MMAs.
 #include "fm_common.cuh"
 
 namespace fm {
@@ -22,12 +22,12 @@ namespace {
 
 constexpr int kTile = 128;
 constexpr int kGroups = 4;    // warpgroups of sums
-constexpr int kThreads = kGroups * 128 + 64;
-constexpr int kListWarp = kGroups * 4, kMmaWarp = kListWarp + 1;
+constexpr int kThreads = kGroups * 128 + 96;
+constexpr int kListWarp = kGroups * 4, kLoadWarp = kListWarp + 1, kMmaWarp = kListWarp + 2;
 constexpr int kSMs = 148;
 constexpr int kBufs = kGroups;  // TMEM score buffers of 128 columns, one per warpgroup
 constexpr int kRing = 8;      // listed items of a reader
-constexpr int kReaders = kGroups + 1;  // the warpgroups of sums, the MMA role
+constexpr int kReaders = kGroups + 2;  // the warpgroups of sums, the load and the MMA role
 constexpr float kNegInf = -__builtin_huge_valf();
 
 struct KeyWeightParams {
@@ -63,7 +63,7 @@ struct KeyWeightSmem {
   static constexpr int kAlloc = kBytes + 1024;
 };
 // An item: .x query-tile entry (qt << 1 | partial), .y query head of the group and flags, .z key tile, .w b << 16 | hk.
-// Each reader has a ring of its own: the MMA role gets every query tile, with kFirst and kLast of its key tile; a
+// Each reader has a ring of its own: the load and MMA roles get every query tile, with kFirst and kLast of its key tile; a
 // warpgroup of sums gets its query tiles, with kLast at its last one of the key tile, or a kLast | kEmpty item if it has none.
 constexpr int kFirst = 1 << 8, kLast = 2 << 8, kEmpty = 4 << 8, kEnd = 8 << 8;
 
@@ -239,9 +239,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   int64_t key_at = -1;  // where it goes
 
   if (warp == kListWarp) {
-    // ------------------------------------------------------- list and load role
+    // ------------------------------------------------------------ list role
     if (lane == 0) {
-      int qi = 0, wk = 0;  // query tiles and key tiles so far
+      int qi = 0;  // query tiles so far
       int pushed[kReaders];
 #pragma unroll
       for (int i = 0; i < kReaders; ++i) pushed[i] = 0;
@@ -287,29 +287,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (bool first = true; ok && more; first = false, ++at) {
           const int cur_hg = hg, cur = entry;
           walk.at += step;
-          more = walk.get(hg, entry);  // (the next entry, in flight during this one's copies)
-          if (first) {
-            const int kb = wk % S::kKBufs;
-            if (wk >= S::kKBufs && !mbar_wait_idle(bar(S::K_EMPTY + kb), (wk / S::kKBufs - 1) & 1, abort_flag)) {
-              ok = false;
-              break;
-            }
-            mbar_arrive_expect_tx(bar(S::K_FULL + kb), S::kTileBytes);
-            for (int c = 0; c < kAtoms; ++c)
-              tma_load_4d(k_s + kb * S::kTileBytes + c * 16384, &tm_k, bar(S::K_FULL + kb), c * 64, hk, kt * kTile, b);
-            ++wk;
-          }
-          const int st = qi % S::kStages;
-          if (qi >= S::kStages && !mbar_wait_idle(bar(S::Q_EMPTY + st), (qi / S::kStages - 1) & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(bar(S::Q_FULL + st), S::kTileBytes);
-          for (int c = 0; c < kAtoms; ++c)
-            tma_load_4d(q_s + st * S::kTileBytes + c * 16384, &tm_q, bar(S::Q_FULL + st), c * 64,
-                        hk * p.q_per_kv + cur_hg, (cur >> 1) * kTile, b);
+          more = walk.get(hg, entry);  // (the next entry, in flight while this one is handed out)
           const int4 e = make_int4(cur, cur_hg | (first ? kFirst : 0) | (more ? 0 : kLast), kt, b_hk);
           push(kGroups, pushed[kGroups], e);
+          push(kGroups + 1, pushed[kGroups + 1], e);
 #pragma unroll
           for (int g = 0; g < kGroups; ++g)
             if (qi % kGroups == g) push(g, pushed[g], make_int4(cur, cur_hg | (at + kGroups >= n_items ? kLast : 0), kt, b_hk));
@@ -322,6 +303,44 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < kReaders; ++i) push(i, pushed[i], make_int4(0, kEnd, 0, 0));
       if (!ok) record_failure(p.status, abort_flag, 61);
+    }
+  } else if (warp == kLoadWarp) {
+    // ------------------------------------------------------------ load role
+    if (lane == 0) {
+      bool ok = true;
+      int qi = 0, wk = 0;
+      for (int it = 0;; ++it) {
+        const int slot = kGroups * kRing + it % kRing;
+        if (!mbar_wait_idle(bar(S::ITEM + slot), (it / kRing) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const int4 e = items[slot];
+        mbar_arrive(bar(S::ITEM_FREE + slot));
+        if (e.y & kEnd) break;
+        const int b = (int)((uint32_t)e.w >> 16), hk = e.w & 0xFFFF;
+        const int kb = wk % S::kKBufs, st = qi % S::kStages;
+        if ((e.y & kFirst) && wk >= S::kKBufs && !mbar_wait_idle(bar(S::K_EMPTY + kb), (wk / S::kKBufs - 1) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (e.y & kFirst) {
+          mbar_arrive_expect_tx(bar(S::K_FULL + kb), S::kTileBytes);
+          for (int c = 0; c < kAtoms; ++c)
+            tma_load_4d(k_s + kb * S::kTileBytes + c * 16384, &tm_k, bar(S::K_FULL + kb), c * 64, hk, e.z * kTile, b);
+          ++wk;
+        }
+        if (qi >= S::kStages && !mbar_wait_idle(bar(S::Q_EMPTY + st), (qi / S::kStages - 1) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        mbar_arrive_expect_tx(bar(S::Q_FULL + st), S::kTileBytes);
+        for (int c = 0; c < kAtoms; ++c)
+          tma_load_4d(q_s + st * S::kTileBytes + c * 16384, &tm_q, bar(S::Q_FULL + st), c * 64,
+                      hk * p.q_per_kv + (e.y & 255), (e.x >> 1) * kTile, b);
+        ++qi;
+      }
+      if (!ok) record_failure(p.status, abort_flag, 64);
       // the copies in flight land before this role ends (a consumer that gave up may leave some unread)
       for (int x = max(wk - S::kKBufs, 0); x < wk; ++x) mbar_wait(bar(S::K_FULL + x % S::kKBufs), (x / S::kKBufs) & 1, never);
       for (int x = max(qi - S::kStages, 0); x < qi; ++x) mbar_wait(bar(S::Q_FULL + x % S::kStages), (x / S::kStages) & 1, never);
@@ -335,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int qi = 0, wk = 0;
       for (int it = 0;; ++it) {
-        const int slot = kGroups * kRing + it % kRing;
+        const int slot = (kGroups + 1) * kRing + it % kRing;
         if (!mbar_wait_idle(bar(S::ITEM + slot), (it / kRing) & 1, abort_flag)) {
           ok = false;
           break;
@@ -377,6 +396,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     int ends = 0;
     bool ok = true;
+    // The first warpgroup adds the others' sums of a key tile when the next one ends: they have long arrived then.
+    auto finish = [&](int end) {
+      const int sb = end & 1;
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(S::SUM_FULL + sb), (end >> 1) & 1, abort_flag)) && ok;
+      const float* others = sum_s + sb * (kGroups - 1) * kTile;
+#pragma unroll
+      for (int g = 0; g < kGroups - 1; ++g) sum += others[g * kTile + r];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(S::SUM_EMPTY + sb));
+      if (step == 1 && key_at >= 0) p.weight[key_at] = p.accumulate ? p.weight[key_at] + sum : sum;
+    };
     int mine = 0;  // query tiles so far
     // LSE of this thread's row of an item's query tile; -inf past n_q (and for rows that see no key): their p is 0
     auto load_lse = [&](const int4& e) {
@@ -470,28 +500,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++mine;
       }
       if (e.y & kLast) {  // the key tile is done: the other warpgroups' sums go to the first
-        sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-        const int sb = ends & 1, turn = ends >> 1;
-        float* others = sum_s + sb * (kGroups - 1) * kTile;
+        const float mine_sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
         if (wg > 0) {
+          const int sb = ends & 1, turn = ends >> 1;
           if (turn > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(S::SUM_EMPTY + sb), (turn - 1) & 1, abort_flag));
-          others[(wg - 1) * kTile + r] = sum;
+          sum_s[(sb * (kGroups - 1) + wg - 1) * kTile + r] = mine_sum;
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(S::SUM_FULL + sb));
         } else {
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(S::SUM_FULL + sb), turn & 1, abort_flag));
-#pragma unroll
-          for (int g = 0; g < kGroups - 1; ++g) sum += others[g * kTile + r];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(S::SUM_EMPTY + sb));
+          if (ends > 0) finish(ends - 1);
+          sum = mine_sum;
           key_at = key < p.n_k ? ((int64_t)b * p.H_kv + hk) * p.weight_stride + key : -1;
-          if (step == 1 && key_at >= 0) p.weight[key_at] = p.accumulate ? p.weight[key_at] + sum : sum;
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) acc[u] = 0.f;
         ++ends;
       }
     }
+    if (wg == 0 && ends > 0 && ok) finish(ends - 1);
     if (!ok && lane == 0) record_failure(p.status, abort_flag, 63);
   }
 
