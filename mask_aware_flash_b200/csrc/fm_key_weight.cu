@@ -118,33 +118,6 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) { 
   return v;
 }
 
-// The items (query head of the group, query tile) of one key tile in their fixed order; CTA `rank` of a cluster
-// of `step` takes items rank, rank + step, ...
-struct ItemWalk {
-  const int32_t* count;    // column count of the first head's list
-  const int32_t* entries;
-  int64_t head_count, head_entries;  // distance to the next head's (0 when all heads share one mask)
-  int heads;
-  int head, n, at;
-  __device__ __forceinline__ void start(int rank) {
-    head = -1;
-    n = 0;
-    at = rank;
-  }
-  // moves to the item `at`; false behind the last one
-  __device__ __forceinline__ bool get(int& hg, int& entry) {
-    while (at >= n) {
-      if (head + 1 >= heads) return false;
-      at -= n;
-      ++head;
-      n = __ldg(count + head * head_count);
-    }
-    hg = head;
-    entry = __ldg(entries + head * head_entries + at);
-    return true;
-  }
-};
-
 // 16 columns of this thread's TMEM lane: the load, and the wait for every load so far (which the registers are tied to, so
 // that none of them is read before it).
 __device__ __forceinline__ void tmem_ld16_start(uint32_t taddr, uint32_t (&r)[16]) {
@@ -240,70 +213,78 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kListWarp) {
     // ------------------------------------------------------------ list role
-    if (lane == 0) {
-      int qi = 0;  // query tiles so far
-      int pushed[kReaders];
+    // The whole warp reads the lists (32 entries at a time: an entry's latency would otherwise pace the kernel), lane 0
+    // hands the items out.
+    int qi = 0;  // query tiles so far
+    int pushed[kReaders];
 #pragma unroll
-      for (int i = 0; i < kReaders; ++i) pushed[i] = 0;
-      bool ok = true;
-      auto push = [&](int reader, int& n, const int4& e) {
+    for (int i = 0; i < kReaders; ++i) pushed[i] = 0;
+    bool ok = true;
+    auto push = [&](int reader, int& n, const int4& e) {
+      if (lane == 0) {
         const int at = reader * kRing + n % kRing;
-        if (n >= kRing && !mbar_wait_idle(bar(S::ITEM_FREE + at), (n / kRing - 1) & 1, abort_flag)) {
-          ok = false;
-          return;
+        ok = ok && (n < kRing || mbar_wait_idle(bar(S::ITEM_FREE + at), (n / kRing - 1) & 1, abort_flag));
+        if (ok) {
+          items[at] = e;
+          mbar_arrive(bar(S::ITEM + at));
         }
-        items[at] = e;
-        mbar_arrive(bar(S::ITEM + at));
-        ++n;
-      };
-      int bh = 0, kt = 0;
-      if (work0 < p.n_work) work_of(p, work0, bh, kt);
-      // rounds of one key tile per CTA, every other one in reverse: the first of a round has its longest list
-      for (int round = 0, w = work0; ok && w < p.n_work; ++round) {
-        int bh_next = 0, kt_next = 0;
-        const int w_next = (round + 1) * work_step + ((round & 1) ? work0 : work_step - 1 - work0);
-        if (w_next < p.n_work) work_of(p, w_next, bh_next, kt_next);  // (in flight until it is used)
-        const int b = bh / p.H_kv, hk = bh % p.H_kv;
-        const int b_hk = (int)((uint32_t)b << 16 | (uint32_t)hk);
-        const int64_t bhm0 = (int64_t)b * p.Hm + (p.Hm == 1 ? 0 : hk * p.q_per_kv);
-        ItemWalk walk;
-        walk.count = p.col_count + bhm0 * p.T_k + kt;
-        walk.entries = p.col_entries + (bhm0 * p.T_k + kt) * p.T_q;
-        walk.head_count = p.Hm == 1 ? 0 : p.T_k;
-        walk.head_entries = p.Hm == 1 ? 0 : (int64_t)p.T_k * p.T_q;
-        walk.heads = p.q_per_kv;
-        // query tiles of this key tile that this CTA takes
-        int total = 0;
-        if (p.Hm == 1) total = __ldg(walk.count) * p.q_per_kv;
-        else
-          for (int h = 0; h < p.q_per_kv; ++h) total += __ldg(walk.count + h * walk.head_count);
-        const int n_items = total > rank ? (total - rank + step - 1) / step : 0;
-        walk.start(rank);
-        int hg, entry, at = 0;
-        bool more = walk.get(hg, entry);
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g)
-          if ((g - qi % kGroups + kGroups) % kGroups >= n_items) push(g, pushed[g], make_int4(0, kLast | kEmpty, kt, b_hk));
-        for (bool first = true; ok && more; first = false, ++at) {
-          const int cur_hg = hg, cur = entry;
-          walk.at += step;
-          more = walk.get(hg, entry);  // (the next entry, in flight while this one is handed out)
-          const int4 e = make_int4(cur, cur_hg | (first ? kFirst : 0) | (more ? 0 : kLast), kt, b_hk);
-          push(kGroups, pushed[kGroups], e);
-          push(kGroups + 1, pushed[kGroups + 1], e);
-#pragma unroll
-          for (int g = 0; g < kGroups; ++g)
-            if (qi % kGroups == g) push(g, pushed[g], make_int4(cur, cur_hg | (at + kGroups >= n_items ? kLast : 0), kt, b_hk));
-          ++qi;
-        }
-        bh = bh_next;
-        kt = kt_next;
-        w = w_next;
       }
+      ++n;
+    };
+    int bh = 0, kt = 0;
+    if (work0 < p.n_work) work_of(p, work0, bh, kt);
+    // rounds of one key tile per CTA, every other one in reverse: the first of a round has its longest list
+    for (int round = 0, w = work0; ok && w < p.n_work; ++round) {
+      int bh_next = 0, kt_next = 0;
+      const int w_next = (round + 1) * work_step + ((round & 1) ? work0 : work_step - 1 - work0);
+      if (w_next < p.n_work) work_of(p, w_next, bh_next, kt_next);  // (in flight until it is used)
+      const int b = bh / p.H_kv, hk = bh % p.H_kv;
+      const int b_hk = (int)((uint32_t)b << 16 | (uint32_t)hk);
+      const int64_t bhm0 = (int64_t)b * p.Hm + (p.Hm == 1 ? 0 : hk * p.q_per_kv);
+      const int32_t* counts = p.col_count + bhm0 * p.T_k + kt;
+      const int32_t* entries = p.col_entries + (bhm0 * p.T_k + kt) * p.T_q;
+      // list lengths of the group's heads (at most 64) in two registers of the lanes, and their sum
+      int n0 = 0, n1 = 0;
+      if (lane < p.q_per_kv) n0 = __ldg(counts + (p.Hm == 1 ? 0 : (int64_t)lane * p.T_k));
+      if (lane + 32 < p.q_per_kv) n1 = __ldg(counts + (p.Hm == 1 ? 0 : (int64_t)(lane + 32) * p.T_k));
+      const int total = __reduce_add_sync(0xffffffffu, n0 + n1);
+      const int n_items = total > rank ? (total - rank + step - 1) / step : 0;  // of this CTA
 #pragma unroll
-      for (int i = 0; i < kReaders; ++i) push(i, pushed[i], make_int4(0, kEnd, 0, 0));
-      if (!ok) record_failure(p.status, abort_flag, 61);
+      for (int g = 0; g < kGroups; ++g)
+        if ((g - qi % kGroups + kGroups) % kGroups >= n_items) push(g, pushed[g], make_int4(0, kLast | kEmpty, kt, b_hk));
+      int item = 0, skip = rank;  // items handed out; entries to pass over before the next one
+      for (int hg = 0; hg < p.q_per_kv; ++hg) {
+        const int n = __shfl_sync(0xffffffffu, hg < 32 ? n0 : n1, hg & 31);
+        const int32_t* list = entries + (p.Hm == 1 ? 0 : (int64_t)hg * p.T_k * p.T_q);
+        int at = skip;
+        for (; at < n; at += 32 * step) {
+          const int mine = at + lane * step < n ? __ldg(list + at + lane * step) : 0;
+          const int here = min(32, (n - at + step - 1) / step);
+          for (int j = 0; j < here; ++j, ++item, ++qi) {
+            const int entry = __shfl_sync(0xffffffffu, mine, j);
+            const int4 e = make_int4(entry, hg | (item == 0 ? kFirst : 0) | (item + 1 == n_items ? kLast : 0), kt, b_hk);
+            push(kGroups, pushed[kGroups], e);
+            push(kGroups + 1, pushed[kGroups + 1], e);
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g)
+              if (qi % kGroups == g) push(g, pushed[g], make_int4(entry, hg | (item + kGroups >= n_items ? kLast : 0), kt, b_hk));
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+          }
+          if (!ok) break;
+        }
+        // the first entry of the next head's list that is this CTA's
+        skip = skip >= n ? skip - n : (step - (n - skip) % step) % step;
+        if (!ok) break;
+      }
+      bh = bh_next;
+      kt = kt_next;
+      w = w_next;
+      ok = __shfl_sync(0xffffffffu, ok, 0);  // (the lanes leave the loop together)
     }
+#pragma unroll
+    for (int i = 0; i < kReaders; ++i) push(i, pushed[i], make_int4(0, kEnd, 0, 0));
+    if (!ok && lane == 0) record_failure(p.status, abort_flag, 61);
   } else if (warp == kLoadWarp) {
     // ------------------------------------------------------------ load role
     if (lane == 0) {
