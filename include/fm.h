@@ -314,7 +314,7 @@ fm_status fm_attn_bwd_noalloc(const fm_attn_args* a, const fm_mask_meta* meta, c
  *   scale is 0 if amax = 0, else the smallest power of two 2^e >= amax / Qmax, e >= -126; codes are
  *   x / scale rounded to nearest, ties to even, after clamping to [-Qmax, Qmax] (so infinities
  *   saturate); NaN becomes 0.  Powers of two make the division exact, so a code has one rounding.
- *   D is 64, 128 or 256; n_pages * H_kv * 64 and B * H_kv * max_pages * 64 are below 2^31; B <= 2048.
+ *   D is 64, 128 or 256; n_pages * H_kv * 64 and B * H_kv * max_pages * 64 are below 2^31; B, H_kv <= 65535.
  */
 typedef struct {
   int32_t B, H_kv, D, n_pages, max_pages;
@@ -357,7 +357,7 @@ typedef struct {
   const int32_t* vec[4]; /* mask vectors LTS, LTE, UTS, UTE, device int32 [B, Hm, n_k], read at each key's pos;
                             NULL: LTS, LTE = 2^31 - 1 (no last row is known here), UTS, UTE = 0.  Keys whose
                             pos lies outside [0, n_k) are masked by no vector. */
-  int32_t Hm, n_k;    /* Hm = 1 or H; both 0 without vectors */
+  int32_t Hm, n_k;    /* Hm = 1 or H (row is needed then); both 0 without vectors */
   int32_t causal;     /* 1: a key is also masked for the rows before its pos */
   int32_t accumulate; /* 1: add the weight each key receives to cache->weight */
 } fm_cache_attn_args;

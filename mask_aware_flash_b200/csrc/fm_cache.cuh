@@ -9,7 +9,7 @@
 namespace fm {
 
 constexpr int kPage = FM_CACHE_PAGE;
-constexpr int kMaxCacheB = 2048;  // sequences: the attention kernel holds their block counts in shared memory
+constexpr int kMaxCacheB = 65535;  // sequences: a grid dimension
 
 // Host checks of a cache's shape and pointers (fm_cache.cu).
 fm_status check_cache(const fm_kv_cache* c);

@@ -3,13 +3,14 @@
 // The path is bound by the bytes of the cache: every live key's K and V codes are read once, 2 D bytes
 // per key and K/V head, and each is used for the n_q * H / H_kv rows that share the head.  So the design
 // starts from the copies:
-//   * the (sequence, K/V head, 64-token block) units of the whole batch form one flat order that is cut
-//     into equal runs, one per CTA (one CTA per SM): ragged lengths and long single sequences load every
-//     SM alike.  A (sequence, head) cut by a run's border is joined by the second kernel.
+//   * blocks that no row sees are found from the mask vectors by a kernel of its own (only where there is a
+//     mask) before anything of them is loaded; it leaves the list of the others.
+//   * the listed (sequence, K/V head, 64-token block) units of the whole batch form one flat order that is
+//     cut into equal runs, one per CTA (one CTA per SM): ragged lengths, sparse masks and long single
+//     sequences load every SM alike.  A (sequence, head) cut by a run's border is joined by the last kernel.
 //   * each warp owns a ring of K and V blocks in shared memory, filled by TMA (64 rows of D codes, 64- or
 //     128-byte swizzle) through mbarriers, and works through its share of the run's blocks alone: no CTA
 //     barrier until a (sequence, head) ends.
-//   * blocks that no row sees are found from the mask vectors before anything of them is loaded.
 // The products run on mma.sync m16n8k16 with fp16 operands and fp32 accumulation, as
 //   S^T [keys x rows] = K Q^T   and   O^T [d x rows] += V^T P^T,
 // so that the 8 columns of the instruction are the few query rows and no row of it is padding for up to
@@ -43,14 +44,17 @@ struct CacheAttnParams {
   __nv_bfloat16* o;
   float* lse;
   // workspace
-  int32_t* units;    // [B + 1] units before each sequence
+  int32_t* units;    // [B * H_kv + 1] units before each (sequence, head)
+  int32_t* chunk_n;  // [B * H_kv][n_chunk] listed blocks of each chunk of blocks (mask)
+  int32_t* listed;   // [B * H_kv][n_chunk][chunk] those blocks, ascending: block << 1 | some row does not see some key (mask)
   float* part_o;     // [n_work][2][n_rows_pad][D] partial sums of runs that end inside a (sequence, head)
   float2* part_ml;   // [n_work][2][n_rows_pad] their running maximum (log2) and sum
   float2* whole_ml;  // [B * H_kv][n_rows_pad] the same for (sequence, head)s inside one run (accumulate)
   float* score;      // [B * H_kv][max_pages * 64][rows4] scores in log2 units (accumulate)
   uint8_t* live;     // [B * H_kv][max_pages] block was read (accumulate)
   int* status;
-  int B, H, H_kv, n_q, group, n_rows, n_rows_pad, rows4, Hm, n_k, n_pages, max_pages, n_work, n_chunks;
+  int B, H, H_kv, n_q, group, n_rows, n_rows_pad, rows4, Hm, n_k, n_pages, max_pages, n_work, n_row_chunks;
+  int n_chunk, chunk;  // chunks of blocks per (sequence, head), blocks of a chunk (n_chunk = 1 without a mask)
   int masked, causal, accumulate;
   float scale_log2;
 };
@@ -59,13 +63,14 @@ template <int D, int NT>
 struct CacheAttnCfg {
   static constexpr int kWarps = D == 256 ? 4 : 8;
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kSlots = D == 64 ? 4 : 2;     // ring slots of a warp (each one K or one V block)
+  // ring slots of a warp (each one K or one V block): what shared memory holds
+  static constexpr int kSlots = NT == 1 ? (D == 64 ? 6 : 3) : (D == 64 ? 4 : 2);
   static constexpr int kBox = D < 128 ? D : 128;     // bytes of a TMA box row (= swizzle span)
   static constexpr int kBoxes = D / kBox;
   static constexpr int kSlotBytes = kPage * D;
   static constexpr int kRows = 8 * NT;               // query rows a CTA holds
   static constexpr int kKSteps = D / 16;
-  static constexpr int kCap = 512;                   // units listed at a time
+  static constexpr int kCap = 256;                   // units listed at a time
   static constexpr int kRing = 0;
   static constexpr int kQ = kRing + kWarps * kSlots * kSlotBytes;       // fragments [NT][D / 16][32] x 8 bytes
   static constexpr int kTree = kQ + NT * kKSteps * 32 * 8;              // [warps / 2][regs][32] fp32
@@ -73,15 +78,17 @@ struct CacheAttnCfg {
   static constexpr int kList = kTree + kWarps / 2 * kRegs * 32 * 4;     // int4 entries
   static constexpr int kSegStart = kList + kCap * 16;                   // int [kCap + 1] (padded)
   static constexpr int kSegBh = kSegStart + (kCap + 4) * 4;             // int [kCap]
-  static constexpr int kSegFlag = kSegBh + kCap * 4;                    // int [kCap]: 1 begins, 2 ends here
-  static constexpr int kCls = kSegFlag + kCap * 4;                      // uint8 [kCap]
-  static constexpr int kMl = kCls + kCap;                               // float2 [warps][rows]
+  static constexpr int kSegFlag = kSegBh + kCap * 4;                    // int [kCap]
+  static constexpr int kUnitBh = kSegFlag + kCap * 4;                   // int [kCap + 2]: of the units, one before and one behind
+  static constexpr int kMl = kUnitBh + (kCap + 4) * 4;                  // float2 [warps][rows]
   static constexpr int kQs = kMl + kWarps * kRows * 8;                  // float [rows]
   static constexpr int kBits = kQs + kRows * 4;                         // uint2 [warps][rows] mask bits
   static constexpr int kBar = kBits + kWarps * kRows * 8;               // mbarriers [warps][slots]
-  static constexpr int kMisc = kBar + kWarps * kSlots * 8;              // abort, zero, scan totals
-  static constexpr int kRed = kMisc + 32;                               // uint32 [32]
-  static constexpr int kUnits = kRed + 128;                             // int [B + 1] (dynamic)
+  static constexpr int kMisc = kBar + kWarps * kSlots * 8;              // abort, zero
+  static constexpr int kRed = kMisc + 16;                               // int [32]
+  static constexpr int kBefore = kRed + 128;                            // int [threads]: units before each thread's lists
+  static constexpr int kBytes = kBefore + kThreads * 4;
+  static constexpr int kAlloc = kBytes + 1024;
 };
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
@@ -135,16 +142,105 @@ __device__ __forceinline__ bool key_seen(const CacheAttnParams& p, const KeyBoun
   return k.in && !(p.causal && k.j > i) && !(k.lts <= i && i < k.lte) && !(k.uts <= i && i < k.ute);
 }
 
-// Sequence of a unit: the largest b with units[b] <= u.
-__device__ __forceinline__ int find_seq(const int* units, int B, int u) {
-  int lo = 0, hi = B - 1;
+// Units of a run: an equal share, but no fewer than the CTA has warps (a block per warp takes no longer than one block, and
+// there are fewer partial sums to join).
+__device__ __forceinline__ int units_per_run(int total, int n_work, int warps) {
+  return max((total + n_work - 1) / n_work, warps);
+}
+
+// The lists of units: list e is chunk e % n_chunk of (sequence, head) e / n_chunk.
+__device__ __forceinline__ int list_len(const CacheAttnParams& p, int e) {
+  if (p.masked) return __ldcg(p.chunk_n + e);
+  return (min(max(__ldg(p.len + e / p.H_kv), 0), p.max_pages * kPage) + kPage - 1) / kPage;
+}
+// List and place in it of unit u.  before[t]: units before list t * per.
+__device__ __forceinline__ int2 find_unit(const CacheAttnParams& p, const int* before, int threads, int per, int u) {
+  int lo = 0, hi = threads - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (units[mid] <= u) lo = mid;
+    if (before[mid] <= u) lo = mid;
     else hi = mid - 1;
   }
-  return lo;
+  int e = lo * per, at = u - before[lo];
+  for (int n = list_len(p, e); at >= n; n = list_len(p, ++e)) at -= n;
+  return make_int2(e, at);
 }
+
+// First kernel of a call with a mask: a CTA classifies one chunk of a (sequence, head)'s blocks and lists those that some row
+// sees.  A warp takes kGang blocks at a time (their loads in flight together), two keys per lane.
+constexpr int kPlanThreads = 256;
+constexpr int kMaxChunk = 1024;
+__global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const CacheAttnParams p) {
+  constexpr int kGang = 4;
+  __shared__ uint8_t cls[kMaxChunk];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int hk = blockIdx.y, b = blockIdx.z;
+  const int64_t bh = (int64_t)b * p.H_kv + hk;
+  const int len = min(max(__ldg(p.len + b), 0), p.max_pages * kPage), nb = (len + kPage - 1) / kPage;
+  const int first = blockIdx.x * p.chunk, n = min(nb - first, p.chunk);
+  const int64_t list = bh * p.n_chunk + blockIdx.x;
+  if (n <= 0) {
+    if (threadIdx.x == 0) p.chunk_n[list] = 0;
+    return;
+  }
+  const int row0 = __ldg(p.row + b), head = b * p.Hm + (p.Hm > 1 ? hk * p.group : 0);
+  for (int x0 = warp * kGang; x0 < n; x0 += kPlanThreads / 32 * kGang) {
+    KeyBounds k[kGang][2];
+    bool any[kGang], all[kGang];
+    int page[kGang];
+#pragma unroll
+    for (int x = 0; x < kGang; ++x) {
+      const int blk = first + min(x0 + x, n - 1);
+      page[x] = __ldg(p.page_table + (int64_t)b * p.max_pages + blk);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) load_pos(p, k[x][i], bh, blk * kPage + lane + 32 * i, len);
+      any[x] = false;
+      all[x] = true;
+    }
+    for (int hg = 0; hg < (p.Hm > 1 ? p.group : 1); ++hg) {
+#pragma unroll
+      for (int x = 0; x < kGang; ++x)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) load_vectors(p, k[x][i], head + hg);
+      for (int tq = 0; tq < p.n_q; ++tq)
+#pragma unroll
+        for (int x = 0; x < kGang; ++x)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const bool s = key_seen(p, k[x][i], row0 + tq);
+            any[x] |= s;
+            all[x] &= s;
+          }
+    }
+#pragma unroll
+    for (int x = 0; x < kGang; ++x) {
+      const bool some = __any_sync(0xffffffffu, any[x]), every = __all_sync(0xffffffffu, all[x]);
+      if (lane == 0 && x0 + x < n) cls[x0 + x] = some && page[x] >= 0 && page[x] < p.n_pages ? (every ? 2 : 1) : 0;
+    }
+  }
+  __syncthreads();
+  if (p.accumulate)
+    for (int x = threadIdx.x; x < n; x += kPlanThreads) p.live[bh * p.max_pages + first + x] = cls[x] != 0;
+  if (warp == 0) {
+    int32_t* out = p.listed + list * p.chunk;
+    int count = 0;
+    for (int x = lane; x - lane < n; x += 32) {
+      const int c = x < n ? cls[x] : 0;
+      const uint32_t there = __ballot_sync(0xffffffffu, c != 0);
+      if (c) out[count + __popc(there & ((1u << lane) - 1u))] = (first + x) << 1 | (c == 1 ? 1 : 0);
+      count += __popc(there);
+    }
+    if (lane == 0) p.chunk_n[list] = count;
+  }
+}
+
+// What a segment (the units of one (sequence, head) in one list of a CTA) is to its CTA and to its (sequence, head).
+constexpr int kReset = 1;   // the CTA's first units of it
+constexpr int kDone = 2;    // the CTA's last ones: its sums are written
+constexpr int kBegin = 4;   // its first units at all
+constexpr int kEndAll = 8;  // its last ones
+constexpr int kInside = 16; // kBegin, and not at the run's first unit
 
 template <int D, int NT, bool E4M3>
 __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
@@ -156,7 +252,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_base_1024(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int work = blockIdx.x / p.n_chunks, chunk = blockIdx.x % p.n_chunks;
+  const int work = blockIdx.x / p.n_row_chunks, chunk = blockIdx.x % p.n_row_chunks;
   const int row_base = chunk * C::kRows;  // first query row of this CTA
 
   uint2* q_s = reinterpret_cast<uint2*>(smem + C::kQ);
@@ -165,15 +261,15 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
   int* seg_start = reinterpret_cast<int*>(smem + C::kSegStart);
   int* seg_bh = reinterpret_cast<int*>(smem + C::kSegBh);
   int* seg_flag = reinterpret_cast<int*>(smem + C::kSegFlag);
-  uint8_t* cls = smem + C::kCls;
+  int* unit_bh = reinterpret_cast<int*>(smem + C::kUnitBh) + 1;  // [-1 .. kCap]
   float2* ml_s = reinterpret_cast<float2*>(smem + C::kMl);
   float* qs_s = reinterpret_cast<float*>(smem + C::kQs);
   uint2* bits_s = reinterpret_cast<uint2*>(smem + C::kBits) + warp * C::kRows;
   int* misc = reinterpret_cast<int*>(smem + C::kMisc);
   volatile int* abort_flag = misc;
   const volatile int* never = misc + 1;
-  uint32_t* red = reinterpret_cast<uint32_t*>(smem + C::kRed);
-  int* units = reinterpret_cast<int*>(smem + C::kUnits);
+  int* red = reinterpret_cast<int*>(smem + C::kRed);
+  int* before = reinterpret_cast<int*>(smem + C::kBefore);
   const uint32_t ring = smem_u32(smem + C::kRing) + warp * kSlots * C::kSlotBytes;
   const uint8_t* ring_p = smem + C::kRing + warp * kSlots * C::kSlotBytes;
   const uint32_t bar0 = smem_u32(smem + C::kBar) + warp * kSlots * 8;
@@ -186,142 +282,114 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
     prefetch_tmap(&tm_v);
   }
   const int cap = p.max_pages * kPage;
-  for (int b = threadIdx.x; b < p.B; b += kThreads)
-    units[b + 1] = (min(max(__ldg(p.len + b), 0), cap) + kPage - 1) / kPage * p.H_kv;
-  __syncthreads();
-  if (warp == 0) {  // prefix sum over the sequences
-    int carry = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      int x = b0 + lane < p.B ? units[b0 + lane + 1] : 0;
+  if (p.masked) asm volatile("griddepcontrol.wait;" ::: "memory");  // the lists (this kernel starts while they are made)
+  // units before each thread's share of the lists, and in all
+  const int n_lists = p.B * p.H_kv * p.n_chunk, lists_per = (n_lists + kThreads - 1) / kThreads;
+  int total;
+  {
+    const int e0 = min((int)threadIdx.x * lists_per, n_lists), e1 = min(e0 + lists_per, n_lists);
+    int mine = 0;
+    for (int e = e0; e < e1; ++e) mine += list_len(p, e);
+    int x = mine;
 #pragma unroll
-      for (int s = 1; s < 32; s <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, s);
-        if (lane >= s) x += y;
-      }
-      if (b0 + lane < p.B) units[b0 + lane + 1] = carry + x;
-      carry += __shfl_sync(0xffffffffu, x, 31);
+    for (int s = 1; s < 32; s <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, s);
+      if (lane >= s) x += y;
     }
-    if (lane == 0) units[0] = 0;
+    if (lane == 31) red[warp] = x;
+    __syncthreads();
+    int pre = x - mine;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) pre += red[w];
+      total += red[w];
+    }
+    before[threadIdx.x] = pre;
+    if (blockIdx.x == 0) {  // for the last kernel
+      for (int e = e0; e < e1; ++e) {
+        if (e % p.n_chunk == 0) p.units[e / p.n_chunk] = pre;
+        pre += list_len(p, e);
+      }
+      if (threadIdx.x == 0) p.units[p.B * p.H_kv] = total;
+    }
+    __syncthreads();
   }
-  __syncthreads();
-  const int total = units[p.B];
-  if (blockIdx.x == 0)
-    for (int b = threadIdx.x; b <= p.B; b += kThreads) p.units[b] = units[b];
-  const int per = (total + p.n_work - 1) / p.n_work;
+  const int per = units_per_run(total, p.n_work, kWarps);
   const int c0 = min((int64_t)work * per, (int64_t)total), c1 = min(c0 + per, total);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   float o[kTiles][NT][4];
   float m[NT][2], l[NT][2];
   float unit_v = 0.f, max_v = 0.f;  // O is held in units of unit_v (the V scale of the last block)
   int item = 0;                     // ring items consumed by this warp so far
+  int begun = 0;                    // flags of the current segment's first units
   bool ok = true;
 
   for (int w0 = c0; w0 < c1; w0 += C::kCap) {
     const int nu = min(C::kCap, c1 - w0);
-    // -------------------------------------------------------- list the run's blocks (the live ones)
+    // ------------------------------------------------------------------------ list the run's next units
     if (w0 != c0) __syncthreads();  // the last list has been read
-    if (p.masked) {
-      // one warp per block, two keys per lane: does any row see any key / every key?
-      for (int u = warp; u < nu; u += kWarps) {
-        const int b = find_seq(units, p.B, w0 + u);
-        const int len = min(max(__ldg(p.len + b), 0), cap), nb = (len + kPage - 1) / kPage;
-        const int rem = w0 + u - units[b], hk = rem / nb, blk = rem % nb;
-        const int64_t bh = (int64_t)b * p.H_kv + hk;
-        const int row0 = __ldg(p.row + b);
-        KeyBounds k[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) load_pos(p, k[i], bh, blk * kPage + lane + 32 * i, len);
-        bool any = false, all = true;
-        const int heads = p.Hm > 1 ? p.group : 1;
-        for (int hg = 0; hg < heads; ++hg) {
-          const int64_t bhm = p.Hm > 1 ? (int64_t)b * p.Hm + hk * p.group + hg : b;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) load_vectors(p, k[i], bhm);
-          for (int tq = 0; tq < p.n_q; ++tq) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const bool s = key_seen(p, k[i], row0 + tq);
-              any |= s;
-              all &= s;
-            }
-          }
-        }
-        any = __any_sync(0xffffffffu, any);
-        all = __all_sync(0xffffffffu, all);
-        if (lane == 0) cls[u] = any ? (all ? 2 : 1) : 0;
-      }
-      __syncthreads();
-    }
-    uint32_t mine = 0;  // live blocks | segment starts << 16 of this thread's units
     constexpr int kPer = C::kCap / kThreads;
-    int4 ent[kPer];
-    int ubh[kPer], uflag[kPer];  // flags: 1 live, 2 first of its segment here, 4 last here, 8 begins, 16 ends
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int u = threadIdx.x * kPer + i;
-      uflag[i] = 0;
-      if (u >= nu) continue;
-      const int b = find_seq(units, p.B, w0 + u);
-      const int len = min(max(__ldg(p.len + b), 0), cap), nb = (len + kPage - 1) / kPage;
-      const int rem = w0 + u - units[b], hk = rem / nb, blk = rem % nb;
-      const int page = __ldg(p.page_table + (int64_t)b * p.max_pages + blk);
-      const bool there = page >= 0 && page < p.n_pages;
-      const int c = !there ? 0 : p.masked ? cls[u] : ((blk + 1) * kPage > len ? 1 : 2);
-      ubh[i] = b * p.H_kv + hk;
-      if (c) {
-        const int at = page * p.H_kv + hk;
-        ent[i] = make_int4(at * kPage, blk * kPage + (c == 1 ? 1 : 0), __float_as_int(__ldg(p.k_scale + at)),
-                           __float_as_int(__ldg(p.v_scale + at)));
-        uflag[i] |= 1;
-      }
-      if (p.accumulate && chunk == 0) p.live[(int64_t)ubh[i] * p.max_pages + blk] = c != 0;
-      if (u == 0 || blk == 0) uflag[i] |= 2;
-      if (u == nu - 1 || blk == nb - 1) uflag[i] |= 4;
-      if (w0 + u == c0 || blk == 0) uflag[i] |= 8;
-      if (w0 + u == c1 - 1 || blk == nb - 1) uflag[i] |= 16;
-      mine += (uflag[i] & 1) + ((uflag[i] & 2) << 15);
-    }
-    uint32_t incl = mine;
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, s);
-      if (lane >= s) incl += y;
-    }
-    if (lane == 31) red[warp] = incl;
-    __syncthreads();
-    uint32_t before = incl - mine, all = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += red[w];
-      all += red[w];
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      if (uflag[i] & 2) {
-        const int k = before >> 16;
-        seg_start[k] = before & 0xFFFFu;
-        seg_bh[k] = ubh[i];
-        seg_flag[k] = (uflag[i] & 8) ? 1 : 0;
-      }
-      before += (uflag[i] & 1) + ((uflag[i] & 2) << 15);
-      if (uflag[i] & 1) list[(before & 0xFFFFu) - 1] = ent[i];
-    }
-    __syncthreads();
-    // "ends here" goes on top once every segment's word is there (segment starts before a unit, its own included)
-    {
-      uint32_t run = incl - mine;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w)
-        if (w < warp) run += red[w];
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        run += (uflag[i] & 1) + ((uflag[i] & 2) << 15);
-        if ((uflag[i] & 4) && (uflag[i] & 16)) seg_flag[(run >> 16) - 1] |= 2;
+      const int u = i * kThreads + threadIdx.x;
+      if (u < nu) {
+        const int2 at = find_unit(p, before, kThreads, lists_per, w0 + u);
+        const int bh = at.x / p.n_chunk, b = bh / p.H_kv, hk = bh - b * p.H_kv;
+        const int len = min(max(__ldg(p.len + b), 0), cap);
+        int blk = at.y, partial = 0;
+        if (p.masked) {
+          const int w = __ldcg(p.listed + (int64_t)at.x * p.chunk + at.y);
+          blk = w >> 1;
+          partial = w & 1;
+        } else {
+          partial = (blk + 1) * kPage > len;
+        }
+        int page = __ldg(p.page_table + (int64_t)b * p.max_pages + blk);
+        const bool there = page >= 0 && page < p.n_pages;
+        if (!there) page = 0;  // read, but no key of it is seen
+        const int row = page * p.H_kv + hk;
+        list[u] = make_int4(row * kPage, blk * kPage + (there ? partial : 3), there ? __float_as_int(__ldg(p.k_scale + row)) : 0,
+                            there ? __float_as_int(__ldg(p.v_scale + row)) : 0);
+        unit_bh[u] = bh;
+        if (p.accumulate && !p.masked && chunk == 0) p.live[(int64_t)bh * p.max_pages + blk] = there;
+        if (u == 0) unit_bh[-1] = w0 > 0 ? find_unit(p, before, kThreads, lists_per, w0 - 1).x / p.n_chunk : -1;
+        if (u == nu - 1) unit_bh[nu] = w0 + nu < total ? find_unit(p, before, kThreads, lists_per, w0 + nu).x / p.n_chunk : -1;
       }
     }
-    const int n_live = all & 0xFFFFu, n_seg = all >> 16;
-    if (threadIdx.x == 0) seg_start[n_seg] = n_live;
     __syncthreads();
+    int n_seg = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {  // segments: runs of units of one (sequence, head)
+      const int u = i * kThreads + threadIdx.x;
+      const bool starts = u < nu && (u == 0 || unit_bh[u] != unit_bh[u - 1]);
+      const uint32_t who = __ballot_sync(0xffffffffu, starts);
+      if (i > 0) __syncthreads();  // (the counts of the units before have been read)
+      if (lane == 0) red[warp] = __popc(who);
+      __syncthreads();
+      int k = n_seg + __popc(who & ((1u << lane) - 1u));
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) k += red[w];
+        n_seg += red[w];
+      }
+      if (starts) {
+        const bool begin = unit_bh[u] != unit_bh[u - 1];
+        seg_start[k] = u;
+        seg_bh[k] = unit_bh[u];
+        seg_flag[k] = (begin || w0 + u == c0 ? kReset : 0) | (begin ? kBegin : 0) | (begin && w0 + u > c0 ? kInside : 0);
+      }
+    }
+    if (threadIdx.x == 0) seg_start[n_seg] = nu;
+    __syncthreads();
+    for (int k = threadIdx.x; k < n_seg; k += kThreads) {
+      const int u = seg_start[k + 1] - 1;  // the segment's last unit
+      const bool end = unit_bh[u] != unit_bh[u + 1];
+      seg_flag[k] |= (end || w0 + u == c1 - 1 ? kDone : 0) | (end ? kEndAll : 0);
+    }
+    __syncthreads();
+    const int n_live = nu;
 
     // ---------------------------------------------------------------- the ring of this warp
     const int n_items = 2 * (n_live > warp ? (n_live - warp + kWarps - 1) / kWarps : 0);
@@ -414,7 +482,8 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
       const int b = bh / p.H_kv, hk = bh % p.H_kv;
       const int len = min(max(__ldg(p.len + b), 0), cap);
       if (sg + 1 < n_seg) load_q(seg_bh[sg + 1]);  // in flight during this segment
-      if (flag & 1) {
+      if (flag & kReset) {
+        begun = flag;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           m[nt][0] = m[nt][1] = kNegInf;
@@ -428,8 +497,8 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
       }
       for (int e = warp + kWarps * (done >> 1); e < e1; e += kWarps) {
         const int4 ent = list[e];
-        const int slot0 = ent.y & ~1;
-        const bool partial = ent.y & 1;
+        const int slot0 = ent.y & ~3;
+        const bool partial = ent.y & 1, missing = ent.y & 2;
         const float ks = __int_as_float(ent.z), vs = __int_as_float(ent.w);
         if (partial) {
           // bit k of row n's word pair: the row sees key k of the block
@@ -453,8 +522,8 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
               if (lane == (n & 31)) bits_s[n] = make_uint2(lo, hi);
             }
           } else {
-            const uint32_t lo = __ballot_sync(0xffffffffu, slot0 + lane < len);
-            const uint32_t hi = __ballot_sync(0xffffffffu, slot0 + lane + 32 < len);
+            const uint32_t lo = __ballot_sync(0xffffffffu, !missing && slot0 + lane < len);
+            const uint32_t hi = __ballot_sync(0xffffffffu, !missing && slot0 + lane + 32 < len);
             if (lane < C::kRows) bits_s[lane] = make_uint2(lo, hi);
           }
           __syncwarp();
@@ -591,7 +660,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
         wait();
         {
           const uint8_t* vb = ring_p + (item + done) % kSlots * C::kSlotBytes;
-          const int valid = len - slot0;
+          const int valid = missing ? 0 : len - slot0;
           constexpr int kWords = C::kBox / 32;  // 32-bit words of a row's piece that belongs to lane group g
 #pragma unroll
           for (int x = 0; x < C::kBoxes; ++x)
@@ -636,7 +705,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
         issue();
         ++done;
       }
-      if (!(flag & 2)) continue;  // goes on in the next list
+      if (!(flag & kDone)) continue;  // goes on in the next list
 
       // -------------------------------------------------- the segment's end: join the warps
 #pragma unroll
@@ -694,10 +763,8 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
         __syncthreads();
       }
       if (warp == 0) {
-        const int nb = (len + kPage - 1) / kPage;
-        const int u0 = units[b] + hk * nb, u1 = u0 + nb;
-        const bool whole = u0 >= c0 && u1 <= c1;
-        const int64_t part = ((int64_t)work * 2 + (u0 > c0 ? 1 : 0)) * p.n_rows_pad;
+        const bool whole = (begun & kBegin) && (flag & kEndAll);
+        const int64_t part = ((int64_t)work * 2 + (begun & kInside ? 1 : 0)) * p.n_rows_pad;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -738,97 +805,134 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
   }
 }
 
-// Second kernel.  The first B * H_kv * n_rows CTAs each join one row of a (sequence, head) that several runs
-// share; the others each add the softmax weights of kWeightSlots keys to the cache's, from the stored scores.
+// Last kernel (it may be resident before the one before ends, so what that wrote is read through L2).  The first CTAs join
+// the rows of the (sequence, head)s that several runs share, a CTA per row; the others add the softmax weights of kWeightSlots keys each to the cache's, from the stored scores.
 constexpr int kJoinThreads = 128;
 constexpr int kWeightSlots = 512;
 constexpr int kMaxRows = 1024;
 
-struct Span {  // the runs that hold a (sequence, head)
-  int u0, first, last;  // last < first: no units
+struct Span {  // the runs that hold a (sequence, head), and where their partial sums are
+  int first, last;     // last < first: no units
+  int64_t part0;    // first row of run `first`'s partial sums; run c > first has them in its first place
 };
-__device__ __forceinline__ Span span_of(const CacheAttnParams& p, int b, int hk) {
-  const int a = p.units[b], z = p.units[b + 1], nb = (z - a) / p.H_kv;
-  const int per = (p.units[p.B] + p.n_work - 1) / p.n_work;
+__device__ __forceinline__ Span span_of(const CacheAttnParams& p, int bh, int warps) {
+  const int u0 = __ldcg(p.units + bh), u1 = __ldcg(p.units + bh + 1);
+  const int per = units_per_run(__ldcg(p.units + p.B * p.H_kv), p.n_work, warps);
   Span s;
-  s.u0 = a + hk * nb;
-  s.first = nb ? s.u0 / per : 0;
-  s.last = nb ? (s.u0 + nb - 1) / per : -1;
+  s.first = u0 / per;
+  s.last = u1 > u0 ? (u1 - 1) / per : s.first - 1;
+  s.part0 = ((int64_t)s.first * 2 + (u0 > s.first * per ? 1 : 0)) * p.n_rows_pad;
   return s;
 }
 __device__ __forceinline__ int64_t part_of(const CacheAttnParams& p, const Span& s, int c) {
-  const int per = (p.units[p.B] + p.n_work - 1) / p.n_work;
-  return ((int64_t)c * 2 + (s.u0 > c * per ? 1 : 0)) * p.n_rows_pad;
+  return c == s.first ? s.part0 : (int64_t)c * 2 * p.n_rows_pad;
+}
+// Maximum and sum of row r over its runs, by a warp (the same order for every caller).
+__device__ __forceinline__ float2 join_ml(const CacheAttnParams& p, const Span& s, int r, int lane) {
+  float m = kNegInf;
+  for (int c = s.first + lane; c <= s.last; c += 32) m = fmaxf(m, __ldcg(&p.part_ml[part_of(p, s, c) + r].x));
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+  const float use = m == kNegInf ? 0.f : m;
+  float l = 0.f;
+  for (int c = s.first + lane; c <= s.last; c += 32) {
+    const float2 v = __ldcg(&p.part_ml[part_of(p, s, c) + r]);
+    l += v.y * ex2(v.x - use);
+  }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+  return make_float2(m, l);
 }
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const CacheAttnParams p) {
+  constexpr int kMainWarps = CacheAttnCfg<D, 1>::kWarps;
   __shared__ float2 ml[kMaxRows];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the first kernel's results
   const int n_join = p.B * p.H_kv * p.n_rows;
   if ((int)blockIdx.x < n_join) {
+    // every warp finds the row's maximum and sum, then adds up every fourth run's part
+    constexpr int kPer = D / 32;  // consecutive d of a lane
+    __shared__ float part[kJoinThreads / 32][D];
     const int bh = blockIdx.x / p.n_rows, r = blockIdx.x % p.n_rows, b = bh / p.H_kv, hk = bh % p.H_kv;
-    const Span s = span_of(p, b, hk);
+    const Span s = span_of(p, bh, kMainWarps);
     if (s.first == s.last) return;  // written by its one run
-    float m = kNegInf, l = 0.f;
-    for (int c = s.first; c <= s.last; ++c) m = fmaxf(m, p.part_ml[part_of(p, s, c) + r].x);
-    const float use = m == kNegInf ? 0.f : m;
-    for (int c = s.first; c <= s.last; ++c) {
-      const float2 v = p.part_ml[part_of(p, s, c) + r];
-      l += v.y * ex2(v.x - use);
-    }
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-    const int h = hk * p.group + r / p.n_q, tq = r % p.n_q;
-    for (int d = threadIdx.x; d < D; d += kJoinThreads) {
-      float x = 0.f;
-      for (int c = s.first; c <= s.last; ++c) {
-        const int64_t at = part_of(p, s, c) + r;
-        x += p.part_o[at * D + d] * ex2(p.part_ml[at].x - use);
+    const float2 t = join_ml(p, s, r, lane);
+    const float use = t.x == kNegInf ? 0.f : t.x, inv = t.y > 0.f ? 1.f / t.y : (t.y == 0.f ? 0.f : t.y);
+    float x[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) x[i] = 0.f;
+#pragma unroll 4
+    for (int c = s.first + warp; c <= s.last; c += kJoinThreads / 32) {
+      const int64_t at = part_of(p, s, c) + r;
+      const float f = ex2(__ldcg(&p.part_ml[at].x) - use);
+      const float2* src = reinterpret_cast<const float2*>(p.part_o + at * D + lane * kPer);
+#pragma unroll
+      for (int i = 0; i < kPer; i += 2) {
+        const float2 v = __ldcg(src + i / 2);
+        x[i] = fmaf(v.x, f, x[i]);
+        x[i + 1] = fmaf(v.y, f, x[i + 1]);
       }
-      p.o[(((int64_t)b * p.n_q + tq) * p.H + h) * D + d] = __float2bfloat16_rn(x * inv);
     }
-    if (threadIdx.x == 0) p.lse[((int64_t)b * p.H + h) * p.n_q + tq] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) part[warp][lane * kPer + i] = x[i];
+    __syncthreads();
+    const int h = hk * p.group + r / p.n_q, tq = r % p.n_q;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (((int64_t)b * p.n_q + tq) * p.H + h) * D);
+    for (int d = threadIdx.x; d < D / 2; d += kJoinThreads) {
+      float y0 = 0.f, y1 = 0.f;
+#pragma unroll
+      for (int w = 0; w < kJoinThreads / 32; ++w) {
+        y0 += part[w][2 * d];
+        y1 += part[w][2 * d + 1];
+      }
+      dst[d] = pack_bf16(y0 * inv, y1 * inv);
+    }
+    if (threadIdx.x == 0) p.lse[((int64_t)b * p.H + h) * p.n_q + tq] = t.y == 0.f ? kNegInf : (t.x + log2f(t.y)) * kLn2;
     return;
   }
   const int cap = p.max_pages * kPage, per_bh = (cap + kWeightSlots - 1) / kWeightSlots;
-  const int w = blockIdx.x - n_join, bh = w / per_bh, s0 = w % per_bh * kWeightSlots, b = bh / p.H_kv, hk = bh % p.H_kv;
+  const int w = blockIdx.x - n_join, bh = w / per_bh, s0 = w % per_bh * kWeightSlots, b = bh / p.H_kv;
   const int len = min(max(__ldg(p.len + b), 0), cap);
   if (s0 >= len) return;
-  const Span s = span_of(p, b, hk);
-  for (int r = threadIdx.x; r < p.rows4; r += kJoinThreads) {
-    float m = 0.f, l = 0.f;
-    if (r < p.n_rows) {
-      if (s.first == s.last) {
-        const float2 v = p.whole_ml[(int64_t)bh * p.n_rows_pad + r];
-        m = v.x;
-        l = v.y;
-      } else {
-        m = kNegInf;
-        for (int c = s.first; c <= s.last; ++c) m = fmaxf(m, p.part_ml[part_of(p, s, c) + r].x);
-        const float use = m == kNegInf ? 0.f : m;
-        for (int c = s.first; c <= s.last; ++c) {
-          const float2 v = p.part_ml[part_of(p, s, c) + r];
-          l += v.y * ex2(v.x - use);
-        }
-      }
-    }
-    ml[r] = make_float2(m == kNegInf ? 0.f : m, l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l));
+  const Span s = span_of(p, bh, kMainWarps);
+  for (int r = warp; r < p.rows4; r += kJoinThreads / 32) {
+    float2 t = make_float2(kNegInf, 0.f);
+    if (r < p.n_rows) t = s.first == s.last ? __ldcg(&p.whole_ml[(int64_t)bh * p.n_rows_pad + r]) : join_ml(p, s, r, lane);
+    if (lane == 0) ml[r] = make_float2(t.x == kNegInf ? 0.f : t.x, t.y > 0.f ? 1.f / t.y : (t.y == 0.f ? 0.f : t.y));
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < kWeightSlots; i += kJoinThreads) {
-    const int slot = s0 + i;
-    if (slot >= len || !p.live[(int64_t)bh * p.max_pages + slot / kPage]) continue;
-    const float4* sc = reinterpret_cast<const float4*>(p.score + ((int64_t)bh * cap + slot) * p.rows4);
-    float x = 0.f;
-    for (int r = 0; r < p.rows4; r += 4) {
-      const float4 v = __ldg(sc + r / 4);
-      // rows behind the last one hold no score: their factor is 0 and their exponent finite
-      x += ex2(v.x - ml[r].x) * ml[r].y;
-      if (r + 1 < p.n_rows) x += ex2(v.y - ml[r + 1].x) * ml[r + 1].y;
-      if (r + 2 < p.n_rows) x += ex2(v.z - ml[r + 2].x) * ml[r + 2].y;
-      if (r + 3 < p.n_rows) x += ex2(v.w - ml[r + 3].x) * ml[r + 3].y;
-    }
-    p.weight[(int64_t)bh * cap + slot] += x;
+  // four keys a thread, their loads in flight together
+  constexpr int kKeys = kWeightSlots / kJoinThreads;
+  float x[kKeys];
+  bool live[kKeys];
+  const float4* sc[kKeys];
+#pragma unroll
+  for (int i = 0; i < kKeys; ++i) {
+    const int slot = s0 + i * kJoinThreads + threadIdx.x;
+    live[i] = slot < len && __ldcg(p.live + (int64_t)bh * p.max_pages + slot / kPage);
+    sc[i] = reinterpret_cast<const float4*>(p.score + ((int64_t)bh * cap + slot) * p.rows4);
+    x[i] = live[i] ? p.weight[(int64_t)bh * cap + slot] : 0.f;
   }
+  for (int r = 0; r < p.rows4; r += 4) {
+    float4 v[kKeys];
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i) v[i] = live[i] ? __ldcg(sc[i] + r / 4) : make_float4(kNegInf, kNegInf, kNegInf, kNegInf);
+    const float2 m0 = ml[r], m1 = ml[r + 1], m2 = ml[r + 2], m3 = ml[r + 3];
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i) {
+      float y = ex2(v[i].x - m0.x) * m0.y;
+      // rows behind the last one hold no score
+      if (r + 1 < p.n_rows) y += ex2(v[i].y - m1.x) * m1.y;
+      if (r + 2 < p.n_rows) y += ex2(v[i].z - m2.x) * m2.y;
+      if (r + 3 < p.n_rows) y += ex2(v[i].w - m3.x) * m3.y;
+      x[i] += y;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kKeys; ++i)
+    if (live[i]) p.weight[(int64_t)bh * cap + s0 + i * kJoinThreads + threadIdx.x] = x[i];
 }
 
 // ------------------------------------------------------------------------------------------- host
@@ -841,8 +945,9 @@ int row_tiles(int D, int n_rows) {
 }
 
 struct Layout {
-  int nt, n_chunks, n_work, n_rows, n_rows_pad, rows4;
-  size_t units, part_o, part_ml, whole_ml, score, live, total;
+  int nt, n_row_chunks, n_work, n_rows, n_rows_pad, rows4;
+  int n_chunk, chunk;
+  size_t units, chunk_n, listed, part_o, part_ml, whole_ml, score, live, total;
 };
 
 Layout layout_of(const fm_kv_cache* c, const fm_cache_attn_args* a) {
@@ -850,11 +955,11 @@ Layout layout_of(const fm_kv_cache* c, const fm_cache_attn_args* a) {
   const size_t bh = (size_t)c->B * c->H_kv;
   L.n_rows = a->n_q * (a->H / c->H_kv);
   L.nt = row_tiles(c->D, L.n_rows);
-  L.n_chunks = (L.n_rows + 8 * L.nt - 1) / (8 * L.nt);
-  L.n_rows_pad = L.n_chunks * 8 * L.nt;
+  L.n_row_chunks = (L.n_rows + 8 * L.nt - 1) / (8 * L.nt);
+  L.n_rows_pad = L.n_row_chunks * 8 * L.nt;
   L.rows4 = (L.n_rows + 3) / 4 * 4;
   const int64_t most = (int64_t)bh * c->max_pages;
-  L.n_work = L.n_chunks >= kSMs ? 1 : kSMs / L.n_chunks;
+  L.n_work = L.n_row_chunks >= kSMs ? 1 : kSMs / L.n_row_chunks;
   if (L.n_work > most) L.n_work = (int)most;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -862,7 +967,13 @@ Layout layout_of(const fm_kv_cache* c, const fm_cache_attn_args* a) {
     at += (bytes + 255) / 256 * 256;
     return r;
   };
-  L.units = take((size_t)(c->B + 1) * 4);
+  L.units = take((bh + 1) * 4);
+  // chunks of 64 blocks, larger ones where that would make more than 8192 lists (every CTA adds up all their lengths)
+  L.chunk = 64;
+  while (L.chunk < kMaxChunk && bh * ((c->max_pages + L.chunk - 1) / L.chunk) > 8192) L.chunk *= 2;
+  L.n_chunk = (c->max_pages + L.chunk - 1) / L.chunk;
+  L.chunk_n = take(bh * L.n_chunk * 4);
+  L.listed = take(bh * L.n_chunk * L.chunk * 4);
   L.part_o = take((size_t)L.n_work * 2 * L.n_rows_pad * c->D * 4);
   L.part_ml = take((size_t)L.n_work * 2 * L.n_rows_pad * 8);
   const bool acc = a->accumulate != 0;
@@ -895,19 +1006,36 @@ bool encode_pool(CUtensorMap* map, const fm_kv_cache* c, const void* base) {
 template <int D, int NT, bool E4M3>
 fm_status launch(const fm_kv_cache* c, const CacheAttnParams& p, cudaStream_t s) {
   using C = CacheAttnCfg<D, NT>;
-  static_assert(C::kUnits + (kMaxCacheB + 1) * 4 + 1024 <= 227 * 1024, "shared memory exceeds the per-CTA limit");
+  static_assert(C::kAlloc <= 227 * 1024, "shared memory exceeds the per-CTA limit");
   CUtensorMap tk, tv;
   if (!encode_pool(&tk, c, c->k_codes) || !encode_pool(&tv, c, c->v_codes)) return FM_ERR_CUDA;
-  constexpr int kMost = C::kUnits + (kMaxCacheB + 1) * 4 + 1024;
-  if (!smem_opt_in<cache_attn_kernel<D, NT, E4M3>>(kMost)) return FM_ERR_CUDA;
-  const int bytes = C::kUnits + (p.B + 1) * 4 + 1024;
-  cache_attn_kernel<D, NT, E4M3><<<p.n_work * p.n_chunks, C::kThreads, bytes, s>>>(tk, tv, p);
-  if (cudaGetLastError() != cudaSuccess) return FM_ERR_CUDA;
+  if (!smem_opt_in<cache_attn_kernel<D, NT, E4M3>>(C::kAlloc)) return FM_ERR_CUDA;
+  // A kernel that follows one of this call starts while that one ends and waits for its results.
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  if (p.masked) {
+    cache_plan_kernel<<<dim3(p.n_chunk, p.H_kv, p.B), kPlanThreads, 0, s>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return FM_ERR_CUDA;
+    cfg.numAttrs = 1;
+  }
+  cfg.gridDim = dim3(p.n_work * p.n_row_chunks);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kAlloc;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, cache_attn_kernel<D, NT, E4M3>, tk, tv, p);
+  if (e != cudaSuccess) return FM_ERR_CUDA;
   const int64_t bh = (int64_t)p.B * p.H_kv;
   int64_t grid = bh * p.n_rows;
   if (p.accumulate) grid += bh * ((p.max_pages * kPage + kWeightSlots - 1) / kWeightSlots);
-  cache_join_kernel<D><<<(unsigned)grid, kJoinThreads, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FM_OK : FM_ERR_CUDA;
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, cache_join_kernel<D>, p);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? FM_OK : FM_ERR_CUDA;
 }
 
 template <int D, bool E4M3>
@@ -941,7 +1069,7 @@ fm_status fm_cache_attn(const fm_kv_cache* c, const fm_cache_attn_args* a, void*
   if (!a->q || !a->len || !o || !lse || (low & 3)) return FM_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(a->q) | reinterpret_cast<uintptr_t>(o)) & 15) return FM_ERR_INVALID_ARG;
   if (vecs && a->Hm == 0) return FM_ERR_INVALID_ARG;
-  if ((vecs || a->causal) && !a->row) return FM_ERR_INVALID_ARG;
+  if ((a->Hm != 0 || a->causal) && !a->row) return FM_ERR_INVALID_ARG;
   const fm::Layout L = fm::layout_of(c, a);
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255) || ws_bytes < L.total) return FM_ERR_WORKSPACE;
   uint8_t* base = static_cast<uint8_t*>(ws);
@@ -964,6 +1092,7 @@ fm_status fm_cache_attn(const fm_kv_cache* c, const fm_cache_attn_args* a, void*
   p.score = reinterpret_cast<float*>(base + L.score);
   p.live = base + L.live;
   p.status = fm::device_status_ptr();
+  p.masked = a->Hm != 0 || a->causal;
   p.B = c->B;
   p.H = a->H;
   p.H_kv = c->H_kv;
@@ -977,8 +1106,11 @@ fm_status fm_cache_attn(const fm_kv_cache* c, const fm_cache_attn_args* a, void*
   p.n_pages = c->n_pages;
   p.max_pages = c->max_pages;
   p.n_work = L.n_work;
-  p.n_chunks = L.n_chunks;
-  p.masked = vecs || a->causal;
+  p.n_chunk = p.masked ? L.n_chunk : 1;
+  p.chunk = L.chunk;
+  p.chunk_n = reinterpret_cast<int32_t*>(base + L.chunk_n);
+  p.listed = reinterpret_cast<int32_t*>(base + L.listed);
+  p.n_row_chunks = L.n_row_chunks;
   p.causal = a->causal;
   p.accumulate = a->accumulate;
   p.scale_log2 = a->scale * fm::kLog2e;
