@@ -54,6 +54,7 @@ struct CacheAttnParams {
   uint8_t* live;     // [B * H_kv][max_pages] block was read (accumulate)
   int* status;
   int B, H, H_kv, n_q, group, n_rows, n_rows_pad, rows4, Hm, n_k, n_pages, max_pages, n_work, n_row_chunks;
+  int run_min;         // units of a run at least
   int n_chunk, chunk;  // chunks of blocks per (sequence, head), blocks of a chunk (n_chunk = 1 without a mask)
   int masked, causal, accumulate;
   float scale_log2;
@@ -61,21 +62,22 @@ struct CacheAttnParams {
 
 template <int D, int NT>
 struct CacheAttnCfg {
-  static constexpr int kWarps = D == 256 ? 4 : 8;
+  static constexpr int kWarps = NT > 1 ? (D == 256 ? 4 : 8) : (D == 256 ? 6 : 12);
   static constexpr int kThreads = kWarps * 32;
   // ring slots of a warp (each one K or one V block): what shared memory holds
-  static constexpr int kSlots = NT == 1 ? (D == 64 ? 6 : 3) : (D == 64 ? 4 : 2);
+  static constexpr int kSlots = D == 64 ? 4 : 2;
   static constexpr int kBox = D < 128 ? D : 128;     // bytes of a TMA box row (= swizzle span)
   static constexpr int kBoxes = D / kBox;
   static constexpr int kSlotBytes = kPage * D;
   static constexpr int kRows = 8 * NT;               // query rows a CTA holds
   static constexpr int kKSteps = D / 16;
-  static constexpr int kCap = 256;                   // units listed at a time
+  static constexpr int kCap = (256 + kThreads - 1) / kThreads * kThreads;  // units listed at a time
+  static constexpr int kTreeWarps = kWarps >= 8 ? 4 : 2;  // warps that hand their sums over at a time
   static constexpr int kRing = 0;
   static constexpr int kQ = kRing + kWarps * kSlots * kSlotBytes;       // fragments [NT][D / 16][32] x 8 bytes
-  static constexpr int kTree = kQ + NT * kKSteps * 32 * 8;              // [warps / 2][regs][32] fp32
+  static constexpr int kTree = kQ + NT * kKSteps * 32 * 8;              // [kTreeWarps][regs][32] fp32
   static constexpr int kRegs = D / 16 * NT * 4;
-  static constexpr int kList = kTree + kWarps / 2 * kRegs * 32 * 4;     // int4 entries
+  static constexpr int kList = kTree + kTreeWarps * kRegs * 32 * 4;     // int4 entries
   static constexpr int kSegStart = kList + kCap * 16;                   // int [kCap + 1] (padded)
   static constexpr int kSegBh = kSegStart + (kCap + 4) * 4;             // int [kCap]
   static constexpr int kSegFlag = kSegBh + kCap * 4;                    // int [kCap]
@@ -117,6 +119,11 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return r;
 }
 
+// Programmatic launches: a kernel of a call starts while the one before it in the stream ends, waits here for that one's
+// results, and lets the next one start.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Bounds of one cached key: its row index and its two masked stretches.
 struct KeyBounds {
   int j, lts, lte, uts, ute;
@@ -144,8 +151,8 @@ __device__ __forceinline__ bool key_seen(const CacheAttnParams& p, const KeyBoun
 
 // Units of a run: an equal share, but no fewer than the CTA has warps (a block per warp takes no longer than one block, and
 // there are fewer partial sums to join).
-__device__ __forceinline__ int units_per_run(int total, int n_work, int warps) {
-  return max((total + n_work - 1) / n_work, warps);
+__device__ __forceinline__ int units_per_run(const CacheAttnParams& p, int total) {
+  return max((total + p.n_work - 1) / p.n_work, p.run_min);
 }
 
 // The lists of units: list e is chunk e % n_chunk of (sequence, head) e / n_chunk.
@@ -173,7 +180,8 @@ constexpr int kMaxChunk = 1024;
 __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const CacheAttnParams p) {
   constexpr int kGang = 4;
   __shared__ uint8_t cls[kMaxChunk];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_wait();
+  grid_launch_next();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int hk = blockIdx.y, b = blockIdx.z;
   const int64_t bh = (int64_t)b * p.H_kv + hk;
@@ -282,7 +290,8 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
     prefetch_tmap(&tm_v);
   }
   const int cap = p.max_pages * kPage;
-  if (p.masked) asm volatile("griddepcontrol.wait;" ::: "memory");  // the lists (this kernel starts while they are made)
+  grid_wait();
+  grid_launch_next();
   // units before each thread's share of the lists, and in all
   const int n_lists = p.B * p.H_kv * p.n_chunk, lists_per = (n_lists + kThreads - 1) / kThreads;
   int total;
@@ -306,19 +315,12 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
       total += red[w];
     }
     before[threadIdx.x] = pre;
-    if (blockIdx.x == 0) {  // for the last kernel
-      for (int e = e0; e < e1; ++e) {
-        if (e % p.n_chunk == 0) p.units[e / p.n_chunk] = pre;
-        pre += list_len(p, e);
-      }
-      if (threadIdx.x == 0) p.units[p.B * p.H_kv] = total;
-    }
     __syncthreads();
   }
-  const int per = units_per_run(total, p.n_work, kWarps);
+  const int per = units_per_run(p, total);
   const int c0 = min((int64_t)work * per, (int64_t)total), c1 = min(c0 + per, total);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
+  if (total == 0 && blockIdx.x == 0)
+    for (int e = threadIdx.x; e <= p.B * p.H_kv; e += kThreads) p.units[e] = 0;
   float o[kTiles][NT][4];
   float m[NT][2], l[NT][2];
   float unit_v = 0.f, max_v = 0.f;  // O is held in units of unit_v (the V scale of the last block)
@@ -331,6 +333,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
     // ------------------------------------------------------------------------ list the run's next units
     if (w0 != c0) __syncthreads();  // the last list has been read
     constexpr int kPer = C::kCap / kThreads;
+    float scale_k[kPer], scale_v[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int u = i * kThreads + threadIdx.x;
@@ -350,43 +353,16 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
         const bool there = page >= 0 && page < p.n_pages;
         if (!there) page = 0;  // read, but no key of it is seen
         const int row = page * p.H_kv + hk;
-        list[u] = make_int4(row * kPage, blk * kPage + (there ? partial : 3), there ? __float_as_int(__ldg(p.k_scale + row)) : 0,
-                            there ? __float_as_int(__ldg(p.v_scale + row)) : 0);
+        *reinterpret_cast<int2*>(&list[u]) = make_int2(row * kPage, blk * kPage + (there ? partial : 3));
         unit_bh[u] = bh;
+        scale_k[i] = there ? __ldg(p.k_scale + row) : 0.f;  // (stored once the ring has started)
+        scale_v[i] = there ? __ldg(p.v_scale + row) : 0.f;
         if (p.accumulate && !p.masked && chunk == 0) p.live[(int64_t)bh * p.max_pages + blk] = there;
-        if (u == 0) unit_bh[-1] = w0 > 0 ? find_unit(p, before, kThreads, lists_per, w0 - 1).x / p.n_chunk : -1;
-        if (u == nu - 1) unit_bh[nu] = w0 + nu < total ? find_unit(p, before, kThreads, lists_per, w0 + nu).x / p.n_chunk : -1;
       }
     }
-    __syncthreads();
-    int n_seg = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {  // segments: runs of units of one (sequence, head)
-      const int u = i * kThreads + threadIdx.x;
-      const bool starts = u < nu && (u == 0 || unit_bh[u] != unit_bh[u - 1]);
-      const uint32_t who = __ballot_sync(0xffffffffu, starts);
-      if (i > 0) __syncthreads();  // (the counts of the units before have been read)
-      if (lane == 0) red[warp] = __popc(who);
-      __syncthreads();
-      int k = n_seg + __popc(who & ((1u << lane) - 1u));
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) k += red[w];
-        n_seg += red[w];
-      }
-      if (starts) {
-        const bool begin = unit_bh[u] != unit_bh[u - 1];
-        seg_start[k] = u;
-        seg_bh[k] = unit_bh[u];
-        seg_flag[k] = (begin || w0 + u == c0 ? kReset : 0) | (begin ? kBegin : 0) | (begin && w0 + u > c0 ? kInside : 0);
-      }
-    }
-    if (threadIdx.x == 0) seg_start[n_seg] = nu;
-    __syncthreads();
-    for (int k = threadIdx.x; k < n_seg; k += kThreads) {
-      const int u = seg_start[k + 1] - 1;  // the segment's last unit
-      const bool end = unit_bh[u] != unit_bh[u + 1];
-      seg_flag[k] |= (end || w0 + u == c1 - 1 ? kDone : 0) | (end ? kEndAll : 0);
+    if (threadIdx.x >= kThreads - 2) {  // the (sequence, head) of the unit before and of the one behind
+      const int u = threadIdx.x == kThreads - 2 ? -1 : nu, at = w0 + u;
+      unit_bh[u] = at >= 0 && at < total ? find_unit(p, before, kThreads, lists_per, at).x / p.n_chunk : -1;
     }
     __syncthreads();
     const int n_live = nu;
@@ -426,7 +402,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
     // query rows of a segment into shared memory as fragments: row n of tile n / 8, scaled by a power of
     // two that puts its largest element into [2^14, 2^15) (exact; bf16's range is wider than fp16's, and
     // elements under 2^-28 of the largest lose low bits, at most 2^-39 of the row's largest)
-    constexpr int kQRows = C::kRows / kWarps > 0 ? C::kRows / kWarps : 1;
+    constexpr int kQRows = (C::kRows + kWarps - 1) / kWarps;
     constexpr int kQElems = D / 32;  // consecutive elements per lane
     uint32_t qreg[kQRows][kQElems / 2];
     auto load_q = [&](int bh) {
@@ -473,7 +449,50 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
         }
       }
     };
-    load_q(seg_bh[0]);
+    load_q(unit_bh[0]);
+    int n_seg = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {  // segments: runs of units of one (sequence, head)
+      const int u = i * kThreads + threadIdx.x;
+      const bool starts = u < nu && (u == 0 || unit_bh[u] != unit_bh[u - 1]);
+      const uint32_t who = __ballot_sync(0xffffffffu, starts);
+      if (i > 0) __syncthreads();  // (the counts of the units before have been read)
+      if (lane == 0) red[warp] = __popc(who);
+      __syncthreads();
+      int k = n_seg + __popc(who & ((1u << lane) - 1u));
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) k += red[w];
+        n_seg += red[w];
+      }
+      if (starts) {
+        const bool begin = unit_bh[u] != unit_bh[u - 1];
+        seg_start[k] = u;
+        seg_bh[k] = unit_bh[u];
+        seg_flag[k] = (begin || w0 + u == c0 ? kReset : 0) | (begin ? kBegin : 0) | (begin && w0 + u > c0 ? kInside : 0);
+      }
+    }
+    if (threadIdx.x == 0) seg_start[n_seg] = nu;
+    __syncthreads();
+    for (int k = threadIdx.x; k < n_seg; k += kThreads) {
+      const int u = seg_start[k + 1] - 1;  // the segment's last unit
+      const bool end = unit_bh[u] != unit_bh[u + 1];
+      seg_flag[k] |= (end || w0 + u == c1 - 1 ? kDone : 0) | (end ? kEndAll : 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int u = i * kThreads + threadIdx.x;
+      if (u < nu) *(reinterpret_cast<float2*>(&list[u]) + 1) = make_float2(scale_k[i], scale_v[i]);
+    }
+    if (blockIdx.x == 0 && w0 == 0) {  // units before each (sequence, head), for the last kernel
+      const int e0 = min((int)threadIdx.x * lists_per, n_lists), e1 = min(e0 + lists_per, n_lists);
+      int pre = before[threadIdx.x];
+      for (int e = e0; e < e1; ++e) {
+        if (e % p.n_chunk == 0) p.units[e / p.n_chunk] = pre;
+        pre += list_len(p, e);
+      }
+      if (threadIdx.x == 0) p.units[p.B * p.H_kv] = total;
+    }
     store_q();
     __syncthreads();
 
@@ -581,7 +600,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
         bool moved = false;
         float alpha[NT][2];
         const float unit_new = vs > 0.f ? fmaxf(vs, fmaxf(max_v, vs) * 9.094947e-13f) : unit_v;  // 2^-40: see below
-        const float p_scale = vs > 0.f ? vs / unit_new : 1.f;
+        const float p_scale = unit_new == vs || vs == 0.f ? 1.f : vs / unit_new;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -640,7 +659,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
         // O moves to this block's maximum and V scale.  The V scale is a common factor of a block's codes, so
         // O is held in units of the last block's; a block more than 2^40 below the largest one seen keeps to
         // 2^-40 of that, its P scaled instead (O would overflow in ever smaller units).
-        const float fu = unit_v > 0.f ? unit_v / unit_new : 1.f;
+        const float fu = unit_v == unit_new || unit_v == 0.f ? 1.f : unit_v / unit_new;
         max_v = fmaxf(max_v, vs);
         unit_v = unit_new;
         if (__any_sync(0xffffffffu, moved || fu != 1.f)) {
@@ -741,15 +760,16 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
             o[i][nt][2 + x] *= f;
           }
         }
+      // warps [lo, lo + h) hand theirs to warps [0, h): whole groups first, then halves
 #pragma unroll
-      for (int h = kWarps / 2; h > 0; h >>= 1) {
-        if (warp >= h && warp < 2 * h) {
+      for (int lo = kWarps - C::kTreeWarps, h = C::kTreeWarps; h > 0;) {
+        if (warp >= lo && warp < lo + h) {
 #pragma unroll
           for (int i = 0; i < kTiles; ++i)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int c = 0; c < 4; ++c) tree[((warp - h) * C::kRegs + (i * NT + nt) * 4 + c) * 32 + lane] = o[i][nt][c];
+              for (int c = 0; c < 4; ++c) tree[((warp - lo) * C::kRegs + (i * NT + nt) * 4 + c) * 32 + lane] = o[i][nt][c];
         }
         __syncthreads();
         if (warp < h) {
@@ -761,6 +781,15 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
               for (int c = 0; c < 4; ++c) o[i][nt][c] += tree[(warp * C::kRegs + (i * NT + nt) * 4 + c) * 32 + lane];
         }
         __syncthreads();
+        if (lo > C::kTreeWarps) {
+          lo -= C::kTreeWarps;
+        } else if (lo == C::kTreeWarps) {
+          h = C::kTreeWarps / 2;
+          lo = h;
+        } else {
+          h /= 2;
+          lo = h;
+        }
       }
       if (warp == 0) {
         const bool whole = (begun & kBegin) && (flag & kEndAll);
@@ -815,9 +844,9 @@ struct Span {  // the runs that hold a (sequence, head), and where their partial
   int first, last;     // last < first: no units
   int64_t part0;    // first row of run `first`'s partial sums; run c > first has them in its first place
 };
-__device__ __forceinline__ Span span_of(const CacheAttnParams& p, int bh, int warps) {
+__device__ __forceinline__ Span span_of(const CacheAttnParams& p, int bh) {
   const int u0 = __ldcg(p.units + bh), u1 = __ldcg(p.units + bh + 1);
-  const int per = units_per_run(__ldcg(p.units + p.B * p.H_kv), p.n_work, warps);
+  const int per = units_per_run(p, __ldcg(p.units + p.B * p.H_kv));
   Span s;
   s.first = u0 / per;
   s.last = u1 > u0 ? (u1 - 1) / per : s.first - 1;
@@ -846,17 +875,17 @@ __device__ __forceinline__ float2 join_ml(const CacheAttnParams& p, const Span& 
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const CacheAttnParams p) {
-  constexpr int kMainWarps = CacheAttnCfg<D, 1>::kWarps;
   __shared__ float2 ml[kMaxRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the first kernel's results
+  grid_wait();
+  grid_launch_next();
   const int n_join = p.B * p.H_kv * p.n_rows;
   if ((int)blockIdx.x < n_join) {
     // every warp finds the row's maximum and sum, then adds up every fourth run's part
     constexpr int kPer = D / 32;  // consecutive d of a lane
     __shared__ float part[kJoinThreads / 32][D];
     const int bh = blockIdx.x / p.n_rows, r = blockIdx.x % p.n_rows, b = bh / p.H_kv, hk = bh % p.H_kv;
-    const Span s = span_of(p, bh, kMainWarps);
+    const Span s = span_of(p, bh);
     if (s.first == s.last) return;  // written by its one run
     const float2 t = join_ml(p, s, r, lane);
     const float use = t.x == kNegInf ? 0.f : t.x, inv = t.y > 0.f ? 1.f / t.y : (t.y == 0.f ? 0.f : t.y);
@@ -896,7 +925,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const CacheAtt
   const int w = blockIdx.x - n_join, bh = w / per_bh, s0 = w % per_bh * kWeightSlots, b = bh / p.H_kv;
   const int len = min(max(__ldg(p.len + b), 0), cap);
   if (s0 >= len) return;
-  const Span s = span_of(p, bh, kMainWarps);
+  const Span s = span_of(p, bh);
   for (int r = warp; r < p.rows4; r += kJoinThreads / 32) {
     float2 t = make_float2(kNegInf, 0.f);
     if (r < p.n_rows) t = s.first == s.last ? __ldcg(&p.whole_ml[(int64_t)bh * p.n_rows_pad + r]) : join_ml(p, s, r, lane);
@@ -1004,28 +1033,31 @@ bool encode_pool(CUtensorMap* map, const fm_kv_cache* c, const void* base) {
 }
 
 template <int D, int NT, bool E4M3>
-fm_status launch(const fm_kv_cache* c, const CacheAttnParams& p, cudaStream_t s) {
+fm_status launch(const fm_kv_cache* c, CacheAttnParams p, cudaStream_t s) {
   using C = CacheAttnCfg<D, NT>;
+  p.run_min = C::kWarps;
   static_assert(C::kAlloc <= 227 * 1024, "shared memory exceeds the per-CTA limit");
   CUtensorMap tk, tv;
   if (!encode_pool(&tk, c, c->k_codes) || !encode_pool(&tv, c, c->v_codes)) return FM_ERR_CUDA;
   if (!smem_opt_in<cache_attn_kernel<D, NT, E4M3>>(C::kAlloc)) return FM_ERR_CUDA;
-  // A kernel that follows one of this call starts while that one ends and waits for its results.
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.stream = s;
   cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cudaError_t e;
   if (p.masked) {
-    cache_plan_kernel<<<dim3(p.n_chunk, p.H_kv, p.B), kPlanThreads, 0, s>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return FM_ERR_CUDA;
-    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(p.n_chunk, p.H_kv, p.B);
+    cfg.blockDim = dim3(kPlanThreads);
+    e = cudaLaunchKernelEx(&cfg, cache_plan_kernel, p);
+    if (e != cudaSuccess) return FM_ERR_CUDA;
   }
   cfg.gridDim = dim3(p.n_work * p.n_row_chunks);
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kAlloc;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, cache_attn_kernel<D, NT, E4M3>, tk, tv, p);
+  e = cudaLaunchKernelEx(&cfg, cache_attn_kernel<D, NT, E4M3>, tk, tv, p);
   if (e != cudaSuccess) return FM_ERR_CUDA;
   const int64_t bh = (int64_t)p.B * p.H_kv;
   int64_t grid = bh * p.n_rows;
@@ -1033,7 +1065,6 @@ fm_status launch(const fm_kv_cache* c, const CacheAttnParams& p, cudaStream_t s)
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, cache_join_kernel<D>, p);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? FM_OK : FM_ERR_CUDA;
 }
