@@ -71,7 +71,7 @@ struct CacheAttnCfg {
   static constexpr int kSlotBytes = kPage * D;
   static constexpr int kRows = 8 * NT;               // query rows a CTA holds
   static constexpr int kKSteps = D / 16;
-  static constexpr int kCap = (256 + kThreads - 1) / kThreads * kThreads;  // units listed at a time
+  static constexpr int kCap = (256 + kThreads - 1) / kThreads * kThreads - 2;  // units listed at a time
   static constexpr int kTreeWarps = kWarps >= 8 ? 4 : 2;  // warps that hand their sums over at a time
   static constexpr int kRing = 0;
   static constexpr int kQ = kRing + kWarps * kSlots * kSlotBytes;       // fragments [NT][D / 16][32] x 8 bytes
@@ -206,11 +206,13 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const CacheAtt
       any[x] = false;
       all[x] = true;
     }
+#pragma unroll 1
     for (int hg = 0; hg < (p.Hm > 1 ? p.group : 1); ++hg) {
 #pragma unroll
       for (int x = 0; x < kGang; ++x)
 #pragma unroll
         for (int i = 0; i < 2; ++i) load_vectors(p, k[x][i], head + hg);
+#pragma unroll 1
       for (int tq = 0; tq < p.n_q; ++tq)
 #pragma unroll
         for (int x = 0; x < kGang; ++x)
@@ -332,14 +334,18 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
     const int nu = min(C::kCap, c1 - w0);
     // ------------------------------------------------------------------------ list the run's next units
     if (w0 != c0) __syncthreads();  // the last list has been read
-    constexpr int kPer = C::kCap / kThreads;
+    constexpr int kPer = (C::kCap + 2) / kThreads;
     float scale_k[kPer], scale_v[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int u = i * kThreads + threadIdx.x;
-      if (u < nu) {
+      const int u = i * kThreads + (int)threadIdx.x - 1;  // -1 and nu: the unit before and the one behind
+      if (u <= nu && (w0 + u < 0 || w0 + u >= total)) unit_bh[u] = -1;
+      else if (u <= nu) {
         const int2 at = find_unit(p, before, kThreads, lists_per, w0 + u);
-        const int bh = at.x / p.n_chunk, b = bh / p.H_kv, hk = bh - b * p.H_kv;
+        const int bh = at.x / p.n_chunk;
+        unit_bh[u] = bh;
+        if (u < 0 || u == nu) continue;
+        const int b = bh / p.H_kv, hk = bh - b * p.H_kv;
         const int len = min(max(__ldg(p.len + b), 0), cap);
         int blk = at.y, partial = 0;
         if (p.masked) {
@@ -354,15 +360,10 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
         if (!there) page = 0;  // read, but no key of it is seen
         const int row = page * p.H_kv + hk;
         *reinterpret_cast<int2*>(&list[u]) = make_int2(row * kPage, blk * kPage + (there ? partial : 3));
-        unit_bh[u] = bh;
         scale_k[i] = there ? __ldg(p.k_scale + row) : 0.f;  // (stored once the ring has started)
         scale_v[i] = there ? __ldg(p.v_scale + row) : 0.f;
         if (p.accumulate && !p.masked && chunk == 0) p.live[(int64_t)bh * p.max_pages + blk] = there;
       }
-    }
-    if (threadIdx.x >= kThreads - 2) {  // the (sequence, head) of the unit before and of the one behind
-      const int u = threadIdx.x == kThreads - 2 ? -1 : nu, at = w0 + u;
-      unit_bh[u] = at >= 0 && at < total ? find_unit(p, before, kThreads, lists_per, at).x / p.n_chunk : -1;
     }
     __syncthreads();
     const int n_live = nu;
@@ -449,12 +450,11 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
         }
       }
     };
-    load_q(unit_bh[0]);
     int n_seg = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {  // segments: runs of units of one (sequence, head)
-      const int u = i * kThreads + threadIdx.x;
-      const bool starts = u < nu && (u == 0 || unit_bh[u] != unit_bh[u - 1]);
+      const int u = i * kThreads + (int)threadIdx.x - 1;
+      const bool starts = u >= 0 && u < nu && (u == 0 || unit_bh[u] != unit_bh[u - 1]);
       const uint32_t who = __ballot_sync(0xffffffffu, starts);
       if (i > 0) __syncthreads();  // (the counts of the units before have been read)
       if (lane == 0) red[warp] = __popc(who);
@@ -481,8 +481,8 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int u = i * kThreads + threadIdx.x;
-      if (u < nu) *(reinterpret_cast<float2*>(&list[u]) + 1) = make_float2(scale_k[i], scale_v[i]);
+      const int u = i * kThreads + (int)threadIdx.x - 1;
+      if (u >= 0 && u < nu) *(reinterpret_cast<float2*>(&list[u]) + 1) = make_float2(scale_k[i], scale_v[i]);
     }
     if (blockIdx.x == 0 && w0 == 0) {  // units before each (sequence, head), for the last kernel
       const int e0 = min((int)threadIdx.x * lists_per, n_lists), e1 = min(e0 + lists_per, n_lists);
@@ -493,14 +493,16 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
       }
       if (threadIdx.x == 0) p.units[p.B * p.H_kv] = total;
     }
-    store_q();
     __syncthreads();
 
-    for (int sg = 0; sg < n_seg; ++sg) {
+#pragma unroll 1
+    for (int sg = -1; sg < n_seg; ++sg) {
+      // the rows of the next segment: loaded here, in flight during this one, stored at the end of the loop's body
+      if (sg + 1 < n_seg) load_q(seg_bh[sg + 1]);
+      if (sg >= 0) {
       const int bh = seg_bh[sg], flag = seg_flag[sg], e1 = seg_start[sg + 1];
       const int b = bh / p.H_kv, hk = bh % p.H_kv;
       const int len = min(max(__ldg(p.len + b), 0), cap);
-      if (sg + 1 < n_seg) load_q(seg_bh[sg + 1]);  // in flight during this segment
       if (flag & kReset) {
         begun = flag;
 #pragma unroll
@@ -558,9 +560,10 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
             for (int c = 0; c < 4; ++c) s[j][nt][c] = 0.f;
         {
           const uint8_t* kb = ring_p + (item + done) % kSlots * C::kSlotBytes;
-#pragma unroll
+          // (not unrolled: the kernel's code is read once by most calls, and its misses cost more than the loop)
+#pragma unroll 1
           for (int x = 0; x < C::kBoxes; ++x)
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < (C::kBox == 128 ? 2 : 1); ++h) {
               // key 16 j + 8 r + g, 16-byte piece 2 t + h (t for D = 64): no two lanes of a quarter warp
               // share a bank under the swizzle
@@ -724,7 +727,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
         issue();
         ++done;
       }
-      if (!(flag & kDone)) continue;  // goes on in the next list
+      if (!(flag & kDone)) break;  // the list's last one: goes on in the next list
 
       // -------------------------------------------------- the segment's end: join the warps
 #pragma unroll
@@ -736,7 +739,6 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
           if (g == 0) ml_s[warp * C::kRows + nt * 8 + 2 * t + x] = make_float2(m[nt][x], l[nt][x]);
         }
       __syncthreads();
-      if (sg + 1 < n_seg) store_q();  // every warp is done with the old rows
       float mj[NT][2], lj[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -761,7 +763,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
           }
         }
       // warps [lo, lo + h) hand theirs to warps [0, h): whole groups first, then halves
-#pragma unroll
+#pragma unroll 1
       for (int lo = kWarps - C::kTreeWarps, h = C::kTreeWarps; h > 0;) {
         if (warp >= lo && warp < lo + h) {
 #pragma unroll
@@ -829,6 +831,9 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
             }
           }
       }
+      }
+      if (sg + 1 < n_seg) store_q();  // (every warp is done with the old rows)
+      __syncthreads();
     }
     item += done;
   }
@@ -837,7 +842,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
 // Last kernel (it may be resident before the one before ends, so what that wrote is read through L2).  The first CTAs join
 // the rows of the (sequence, head)s that several runs share, a CTA per row; the others add the softmax weights of kWeightSlots keys each to the cache's, from the stored scores.
 constexpr int kJoinThreads = 128;
-constexpr int kWeightSlots = 512;
+constexpr int kWeightSlots = 2048;
 constexpr int kMaxRows = 1024;
 
 struct Span {  // the runs that hold a (sequence, head), and where their partial sums are
@@ -933,35 +938,39 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const CacheAtt
   }
   __syncthreads();
   // four keys a thread, their loads in flight together
-  constexpr int kKeys = kWeightSlots / kJoinThreads;
-  float x[kKeys];
-  bool live[kKeys];
-  const float4* sc[kKeys];
-#pragma unroll
-  for (int i = 0; i < kKeys; ++i) {
-    const int slot = s0 + i * kJoinThreads + threadIdx.x;
-    live[i] = slot < len && __ldcg(p.live + (int64_t)bh * p.max_pages + slot / kPage);
-    sc[i] = reinterpret_cast<const float4*>(p.score + ((int64_t)bh * cap + slot) * p.rows4);
-    x[i] = live[i] ? p.weight[(int64_t)bh * cap + slot] : 0.f;
-  }
-  for (int r = 0; r < p.rows4; r += 4) {
-    float4 v[kKeys];
-#pragma unroll
-    for (int i = 0; i < kKeys; ++i) v[i] = live[i] ? __ldcg(sc[i] + r / 4) : make_float4(kNegInf, kNegInf, kNegInf, kNegInf);
-    const float2 m0 = ml[r], m1 = ml[r + 1], m2 = ml[r + 2], m3 = ml[r + 3];
+  constexpr int kKeys = 4;
+#pragma unroll 1
+  for (int s1 = s0; s1 < min(s0 + kWeightSlots, len); s1 += kKeys * kJoinThreads) {
+    float x[kKeys];
+    bool live[kKeys];
 #pragma unroll
     for (int i = 0; i < kKeys; ++i) {
-      float y = ex2(v[i].x - m0.x) * m0.y;
-      // rows behind the last one hold no score
-      if (r + 1 < p.n_rows) y += ex2(v[i].y - m1.x) * m1.y;
-      if (r + 2 < p.n_rows) y += ex2(v[i].z - m2.x) * m2.y;
-      if (r + 3 < p.n_rows) y += ex2(v[i].w - m3.x) * m3.y;
-      x[i] += y;
+      const int slot = s1 + i * kJoinThreads + threadIdx.x;
+      live[i] = slot < len && __ldcg(p.live + (int64_t)bh * p.max_pages + slot / kPage);
+      x[i] = live[i] ? p.weight[(int64_t)bh * cap + slot] : 0.f;
     }
-  }
+    const float4* sc = reinterpret_cast<const float4*>(p.score + ((int64_t)bh * cap + s1 + threadIdx.x) * p.rows4);
+#pragma unroll 1
+    for (int r = 0; r < p.rows4; r += 4) {
+      float4 v[kKeys];
 #pragma unroll
-  for (int i = 0; i < kKeys; ++i)
-    if (live[i]) p.weight[(int64_t)bh * cap + s0 + i * kJoinThreads + threadIdx.x] = x[i];
+      for (int i = 0; i < kKeys; ++i)
+        v[i] = live[i] ? __ldcg(sc + (i * kJoinThreads * p.rows4 + r) / 4) : make_float4(kNegInf, kNegInf, kNegInf, kNegInf);
+      const float2 m0 = ml[r], m1 = ml[r + 1], m2 = ml[r + 2], m3 = ml[r + 3];
+#pragma unroll
+      for (int i = 0; i < kKeys; ++i) {
+        float y = ex2(v[i].x - m0.x) * m0.y;
+        // rows behind the last one hold no score
+        if (r + 1 < p.n_rows) y += ex2(v[i].y - m1.x) * m1.y;
+        if (r + 2 < p.n_rows) y += ex2(v[i].z - m2.x) * m2.y;
+        if (r + 3 < p.n_rows) y += ex2(v[i].w - m3.x) * m3.y;
+        x[i] += y;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i)
+      if (live[i]) p.weight[(int64_t)bh * cap + s1 + i * kJoinThreads + threadIdx.x] = x[i];
+  }
 }
 
 // ------------------------------------------------------------------------------------------- host
