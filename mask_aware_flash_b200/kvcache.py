@@ -20,10 +20,11 @@ As everywhere in the package the caller owns the buffers; work runs on the curre
 from __future__ import annotations
 
 import ctypes
+import sys
 
 import torch
 
-from . import (FM_ERR_INVALID_ARG, FM_ERR_UNSUPPORTED, FM_ERR_WORKSPACE, AttnArgs, CacheAttnArgs, FmError, KVCacheC,
+from . import (FM_ERR_INVALID_ARG, FM_ERR_UNSUPPORTED, AttnArgs, CacheAttnArgs, FmError, KVCacheC,
                MaskMeta, VecArray, _check, _check_tensors, _vecs)
 from . import __name__ as _pkg_name
 
@@ -34,7 +35,6 @@ _NO_VECS = VecArray(None, None, None, None)
 
 
 def _lib():
-    import sys
     return sys.modules[_pkg_name].lib()
 
 
@@ -43,12 +43,22 @@ def _call(fn, what, device, stream, *args):
     the current device for the call (a launch goes to the current device)."""
     if stream is not None and not torch.cuda.is_available():
         return _check(fn(*args, stream.cuda_stream), what)
-    if device.index is not None and device.index != torch.cuda.current_device():
+    index = device.index
+    # (the raw handles: a Stream object per call would cost more than the launch it is for)
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        code = fn(*args, raw)
+    else:
         with torch.cuda.device(device):
-            s = torch.cuda.current_stream() if stream is None else stream
-            return _check(fn(*args, s.cuda_stream), what)
-    s = torch.cuda.current_stream() if stream is None else stream
-    return _check(fn(*args, s.cuda_stream), what)
+            code = fn(*args, raw)
+    if code:
+        _check(code, what)
+
+
+def _expect(what, device, name, t, dtype, shape):
+    """One tensor of a call: on `device`, contiguous, of that type and shape (_check_tensors words the error)."""
+    if not (t.is_cuda and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+        _check_tensors(what, device, [(name, t, dtype, shape)])
 
 
 class KVCache:
@@ -82,6 +92,7 @@ class KVCache:
         self.page_table, self.weight, self.pos = page_table, weight, pos
         self.B, self.H_kv, self.D, self.n_pages, self.max_pages = B, H_kv, D, n_pages, max_pages
         self.device = k_codes.device
+        self.batch = (B,)
         self.c = KVCacheC(B, H_kv, D, n_pages, max_pages, _CODE_TYPES[k_codes.dtype], k_codes.data_ptr(),
                           v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), page_table.data_ptr(),
                           None if weight is None else weight.data_ptr(), None if pos is None else pos.data_ptr())
@@ -117,9 +128,14 @@ def fm_cache_append(cache: KVCache, k, v, start, count=None, row=None, stream=No
     what = "fm_cache_append"
     if k.dim() != 4 or k.dtype not in _DTYPES:
         raise FmError(FM_ERR_INVALID_ARG, f"{what}: k must be bfloat16 or float32 [B, n_new, H_kv, D]")
-    B, shape = cache.B, (cache.B, k.shape[1], cache.H_kv, cache.D)
-    _check_tensors(what, cache.device, [("k", k, None, shape), ("v", v, k.dtype, shape), ("start", start, torch.int32, (B,)),
-                                        ("count", count, torch.int32, (B,)), ("row", row, torch.int32, (B,))])
+    dev, batch, shape = cache.device, cache.batch, (cache.B, k.shape[1], cache.H_kv, cache.D)
+    _expect(what, dev, "k", k, k.dtype, shape)
+    _expect(what, dev, "v", v, k.dtype, shape)
+    _expect(what, dev, "start", start, torch.int32, batch)
+    if count is not None:
+        _expect(what, dev, "count", count, torch.int32, batch)
+    if row is not None:
+        _expect(what, dev, "row", row, torch.int32, batch)
     _call(_lib().fm_cache_append, what, cache.device, stream, cache._ref, k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype],
           shape[1], start.data_ptr(), _ptr(count), _ptr(row))
 
@@ -135,7 +151,9 @@ def _attn_args(what, cache, q, cache_len, scale, row, vecs, causal, accumulate):
             if ref.dim() != 3:
                 raise FmError(FM_ERR_INVALID_ARG, f"{what}: vectors must be [B, Hm, n_k]")
             Hm, n_k = ref.shape[1], ref.shape[2]
-            _check_tensors(what, cache.device, [(f"vecs[{c}]", vecs[c], torch.int32, (cache.B, Hm, n_k)) for c in range(4)])
+            for c in range(4):
+                if vecs[c] is not None:
+                    _expect(what, cache.device, f"vecs[{c}]", vecs[c], torch.int32, (cache.B, Hm, n_k))
             vec = _vecs(vecs)
     return CacheAttnArgs(q.shape[2], q.shape[1], 0, scale, q.data_ptr(), _ptr(cache_len), _ptr(row), vec, Hm, n_k,
                          1 if causal else 0, 1 if accumulate else 0)
@@ -158,15 +176,23 @@ def fm_cache_attn(cache: KVCache, q, cache_len, scale, row=None, vecs=None, caus
     fm_cache_attn_workspace_bytes (allocated here when None); calls that may overlap need one each."""
     what = "fm_cache_attn"
     a = _attn_args(what, cache, q, cache_len, scale, row, vecs, causal, accumulate)
-    B, n_q, H, D = shape = tuple(q.shape)
+    dev, batch = cache.device, cache.batch
+    _, n_q, H, _ = q.shape
+    shape, rows = (cache.B, n_q, H, cache.D), (cache.B, H, n_q)
+    _expect(what, dev, "q", q, torch.bfloat16, shape)
+    _expect(what, dev, "cache_len", cache_len, torch.int32, batch)
+    if row is not None:
+        _expect(what, dev, "row", row, torch.int32, batch)
     if o is None:
         o = torch.empty_like(q)
+    else:
+        _expect(what, dev, "o", o, torch.bfloat16, shape)
     if lse is None:
-        lse = torch.empty((B, H, n_q), dtype=torch.float32, device=q.device)
-    _check_tensors(what, cache.device,
-                   [("q", q, None, (cache.B, n_q, H, cache.D)), ("cache_len", cache_len, torch.int32, (B,)),
-                    ("row", row, torch.int32, (B,)), ("o", o, torch.bfloat16, shape),
-                    ("lse", lse, torch.float32, (B, H, n_q)), ("ws", ws, torch.uint8, None)])
+        lse = torch.empty(rows, dtype=torch.float32, device=dev)
+    else:
+        _expect(what, dev, "lse", lse, torch.float32, rows)
+    if ws is not None:
+        _expect(what, dev, "ws", ws, torch.uint8, ws.shape)
     L, ref = _lib(), ctypes.byref(a)
     if ws is None:
         ws = torch.empty(max(int(L.fm_cache_attn_workspace_bytes(cache._ref, ref)), 1), dtype=torch.uint8, device=q.device)
@@ -191,11 +217,14 @@ def fm_attn_key_weight(q, k, lse, meta: MaskMeta, vecs, scale, weight=None, accu
         weight = torch.empty((B, H_kv, n_k), dtype=torch.float32, device=q.device)
     if weight.dim() != 3 or weight.shape[2] < n_k:
         raise FmError(FM_ERR_INVALID_ARG, f"{what}: weight must be [B, H_kv, >= n_k]")
-    d = meta.desc
-    _check_tensors(what, q.device,
-                   [("q", q, None, None), ("k", k, q.dtype, (B, n_k, H_kv, D)), ("lse", lse, torch.float32, (B, H, n_q)),
-                    ("weight", weight, torch.float32, (B, H_kv, weight.shape[2]))] +
-                   [(f"vecs[{c}]", vecs[c], torch.int32, (d.B, d.Hm, d.n_k)) for c in range(4)])
+    d, dev = meta.desc, q.device
+    _expect(what, dev, "q", q, torch.bfloat16, q.shape)
+    _expect(what, dev, "k", k, torch.bfloat16, (B, n_k, H_kv, D))
+    _expect(what, dev, "lse", lse, torch.float32, (B, H, n_q))
+    _expect(what, dev, "weight", weight, torch.float32, (B, H_kv, weight.shape[2]))
+    for c in range(4):
+        if vecs[c] is not None:
+            _expect(what, dev, f"vecs[{c}]", vecs[c], torch.int32, (d.B, d.Hm, d.n_k))
     a = AttnArgs(B, H, n_q, n_k, D, 0, scale, q.data_ptr(), k.data_ptr(), None, H_kv, 0)
     _call(_lib().fm_attn_key_weight, what, q.device, stream, ctypes.byref(a), ctypes.byref(meta.c), _vecs(vecs),
           lse.data_ptr(), weight.data_ptr(), weight.shape[2], 1 if accumulate else 0)
@@ -218,15 +247,17 @@ def fm_cache_evict(src: KVCache, dst: KVCache, cache_len, budget: int, recent: i
         raise FmError(FM_ERR_INVALID_ARG, f"{what}: src and dst must agree in B, H_kv, D and code type")
     if new_len is None:
         new_len = torch.empty_like(cache_len)
-    _check_tensors(what, src.device, [("cache_len", cache_len, torch.int32, (src.B,)),
-                                      ("new_len", new_len, torch.int32, (src.B,)), ("ws", ws, torch.uint8, None),
-                                      ("dst.k_codes", dst.k_codes, None, None)])
+    dev = src.device
+    _expect(what, dev, "cache_len", cache_len, torch.int32, src.batch)
+    _expect(what, dev, "new_len", new_len, torch.int32, src.batch)
+    if ws is not None:
+        _expect(what, dev, "ws", ws, torch.uint8, ws.shape)
+    if dst.device != dev:
+        raise FmError(FM_ERR_INVALID_ARG, f"{what}: src and dst must be on one device")
     L = _lib()
     if ws is None:
         n = int(L.fm_cache_evict_workspace_bytes(src._ref, int(budget)))
         ws = torch.empty(max(n, 1), dtype=torch.uint8, device=src.device)
-    elif ws.numel() < int(L.fm_cache_evict_workspace_bytes(src._ref, int(budget))):
-        raise FmError(FM_ERR_WORKSPACE, f"{what}: workspace too small")
     _call(L.fm_cache_evict, what, src.device, stream, src._ref, dst._ref, cache_len.data_ptr(), int(budget), int(recent),
           new_len.data_ptr(), ws.data_ptr(), ws.numel())
     return new_len
