@@ -62,7 +62,7 @@ struct CacheAttnParams {
 
 template <int D, int NT>
 struct CacheAttnCfg {
-  static constexpr int kWarps = NT > 1 ? (D == 256 ? 4 : 8) : (D == 256 ? 6 : 12);
+  static constexpr int kWarps = D == 256 ? 4 : 8;
   static constexpr int kThreads = kWarps * 32;
   // ring slots of a warp (each one K or one V block): what shared memory holds
   static constexpr int kSlots = D == 64 ? 4 : 2;
@@ -72,18 +72,18 @@ struct CacheAttnCfg {
   static constexpr int kRows = 8 * NT;               // query rows a CTA holds
   static constexpr int kKSteps = D / 16;
   static constexpr int kCap = (256 + kThreads - 1) / kThreads * kThreads - 2;  // units listed at a time
-  static constexpr int kTreeWarps = kWarps >= 8 ? 4 : 2;  // warps that hand their sums over at a time
   static constexpr int kRing = 0;
   static constexpr int kQ = kRing + kWarps * kSlots * kSlotBytes;       // fragments [NT][D / 16][32] x 8 bytes
-  static constexpr int kTree = kQ + NT * kKSteps * 32 * 8;              // [kTreeWarps][regs][32] fp32
+  static constexpr int kJoin = kQ + NT * kKSteps * 32 * 8;              // [warps][regs][32] fp32
   static constexpr int kRegs = D / 16 * NT * 4;
-  static constexpr int kList = kTree + kTreeWarps * kRegs * 32 * 4;     // int4 entries
+  static constexpr int kList = kJoin + kWarps * kRegs * 32 * 4;         // int4 entries
   static constexpr int kSegStart = kList + kCap * 16;                   // int [kCap + 1] (padded)
   static constexpr int kSegBh = kSegStart + (kCap + 4) * 4;             // int [kCap]
   static constexpr int kSegFlag = kSegBh + kCap * 4;                    // int [kCap]
   static constexpr int kUnitBh = kSegFlag + kCap * 4;                   // int [kCap + 2]: of the units, one before and one behind
   static constexpr int kMl = kUnitBh + (kCap + 4) * 4;                  // float2 [warps][rows]
-  static constexpr int kQs = kMl + kWarps * kRows * 8;                  // float [rows]
+  static constexpr int kUv = kMl + kWarps * kRows * 8;                  // float [warps]: the units of their O
+  static constexpr int kQs = kUv + kWarps * 4;                          // float [rows]
   static constexpr int kBits = kQs + kRows * 4;                         // uint2 [warps][rows] mask bits
   static constexpr int kBar = kBits + kWarps * kRows * 8;               // mbarriers [warps][slots]
   static constexpr int kMisc = kBar + kWarps * kSlots * 8;              // abort, zero
@@ -266,13 +266,14 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
   const int row_base = chunk * C::kRows;  // first query row of this CTA
 
   uint2* q_s = reinterpret_cast<uint2*>(smem + C::kQ);
-  float* tree = reinterpret_cast<float*>(smem + C::kTree);
+  float* join = reinterpret_cast<float*>(smem + C::kJoin);
   int4* list = reinterpret_cast<int4*>(smem + C::kList);
   int* seg_start = reinterpret_cast<int*>(smem + C::kSegStart);
   int* seg_bh = reinterpret_cast<int*>(smem + C::kSegBh);
   int* seg_flag = reinterpret_cast<int*>(smem + C::kSegFlag);
   int* unit_bh = reinterpret_cast<int*>(smem + C::kUnitBh) + 1;  // [-1 .. kCap]
   float2* ml_s = reinterpret_cast<float2*>(smem + C::kMl);
+  float* uv_s = reinterpret_cast<float*>(smem + C::kUv);
   float* qs_s = reinterpret_cast<float*>(smem + C::kQs);
   uint2* bits_s = reinterpret_cast<uint2*>(smem + C::kBits) + warp * C::kRows;
   int* misc = reinterpret_cast<int*>(smem + C::kMisc);
@@ -731,105 +732,55 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
 
       // -------------------------------------------------- the segment's end: join the warps
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
 #pragma unroll
           for (int y = 4; y < 32; y <<= 1) l[nt][x] += __shfl_xor_sync(0xffffffffu, l[nt][x], y);
           if (g == 0) ml_s[warp * C::kRows + nt * 8 + 2 * t + x] = make_float2(m[nt][x], l[nt][x]);
         }
-      __syncthreads();
-      float mj[NT][2], lj[NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float mm = kNegInf, ll = 0.f;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, ml_s[w * C::kRows + nt * 8 + 2 * t + x].x);
-          const float use = mm == kNegInf ? 0.f : mm;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float2 v = ml_s[w * C::kRows + nt * 8 + 2 * t + x];
-            ll += v.y * ex2(v.x - use);
-          }
-          mj[nt][x] = mm;
-          lj[nt][x] = ll;
-          const float f = ex2(m[nt][x] - use) * unit_v;
-#pragma unroll
-          for (int i = 0; i < kTiles; ++i) {
-            o[i][nt][x] *= f;
-            o[i][nt][2 + x] *= f;
-          }
-        }
-      // warps [lo, lo + h) hand theirs to warps [0, h): whole groups first, then halves
-#pragma unroll 1
-      for (int lo = kWarps - C::kTreeWarps, h = C::kTreeWarps; h > 0;) {
-        if (warp >= lo && warp < lo + h) {
-#pragma unroll
-          for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int c = 0; c < 4; ++c) tree[((warp - lo) * C::kRegs + (i * NT + nt) * 4 + c) * 32 + lane] = o[i][nt][c];
-        }
-        __syncthreads();
-        if (warp < h) {
-#pragma unroll
-          for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int c = 0; c < 4; ++c) o[i][nt][c] += tree[(warp * C::kRegs + (i * NT + nt) * 4 + c) * 32 + lane];
-        }
-        __syncthreads();
-        if (lo > C::kTreeWarps) {
-          lo -= C::kTreeWarps;
-        } else if (lo == C::kTreeWarps) {
-          h = C::kTreeWarps / 2;
-          lo = h;
-        } else {
-          h /= 2;
-          lo = h;
-        }
+          for (int c = 0; c < 4; ++c) join[(warp * C::kRegs + (i * NT + nt) * 4 + c) * 32 + lane] = o[i][nt][c];
       }
-      if (warp == 0) {
-        const bool whole = (begun & kBegin) && (flag & kEndAll);
-        const int64_t part = ((int64_t)work * 2 + (begun & kInside ? 1 : 0)) * p.n_rows_pad;
+      if (lane == 0) uv_s[warp] = unit_v;
+      __syncthreads();
+      // each warp adds up a share of the accumulators' places (pairs: the same row, d and d + 1) over the warps, in order
+      const bool whole = (begun & kBegin) && (flag & kEndAll);
+      const int64_t part = ((int64_t)work * 2 + (begun & kInside ? 1 : 0)) * p.n_rows_pad;
+#pragma unroll 1
+      for (int pair = warp; pair < C::kRegs / 2; pair += kWarps) {
+        const int x = pair & 1, nt = pair / 2 % NT, i = pair / (2 * NT);
+        const int n = nt * 8 + 2 * t + x, r = row_base + n;
+        float mm = kNegInf;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, ml_s[w * C::kRows + n].x);
+        const float use = mm == kNegInf ? 0.f : mm;
+        float ll = 0.f, y0 = 0.f, y1 = 0.f;
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int r = row_base + nt * 8 + 2 * t + x;
-            const float ll = lj[nt][x];
-            if (whole) {
-              if (r >= p.n_rows) continue;
-              const int h = hk * p.group + r / p.n_q, tq = r % p.n_q;
-              const float inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);  // (a NaN stays one)
-              __nv_bfloat16* dst = p.o + (((int64_t)b * p.n_q + tq) * p.H + h) * D;
-#pragma unroll
-              for (int i = 0; i < kTiles; i += 4) {  // tiles i .. i + 3: 8 consecutive d of this lane's piece
-                const int d = i / (C::kBox / 16) * C::kBox + g * (C::kBox / 8) + 2 * (i % (C::kBox / 16));
-                st_global_v4(dst + d, pack_bf16(o[i][nt][x] * inv, o[i][nt][2 + x] * inv),
-                             pack_bf16(o[i + 1][nt][x] * inv, o[i + 1][nt][2 + x] * inv),
-                             pack_bf16(o[i + 2][nt][x] * inv, o[i + 2][nt][2 + x] * inv),
-                             pack_bf16(o[i + 3][nt][x] * inv, o[i + 3][nt][2 + x] * inv));
-              }
-              if (g == 0) {
-                p.lse[((int64_t)b * p.H + h) * p.n_q + tq] = (mj[nt][x] + log2f(ll)) * kLn2;
-                if (p.accumulate) p.whole_ml[(int64_t)bh * p.n_rows_pad + r] = make_float2(mj[nt][x], ll);
-              }
-            } else {
-              float* dst = p.part_o + (part + r) * D;
-#pragma unroll
-              for (int i = 0; i < kTiles; i += 2) {
-                const int d = i / (C::kBox / 16) * C::kBox + g * (C::kBox / 8) + 2 * (i % (C::kBox / 16));
-                *reinterpret_cast<float4*>(dst + d) =
-                    make_float4(o[i][nt][x], o[i][nt][2 + x], o[i + 1][nt][x], o[i + 1][nt][2 + x]);
-              }
-              if (g == 0) p.part_ml[part + r] = make_float2(mj[nt][x], ll);
-            }
+        for (int w = 0; w < kWarps; ++w) {
+          const float2 v = ml_s[w * C::kRows + n];
+          const float f = ex2(v.x - use), fo = f * uv_s[w];
+          const float* src = join + (w * C::kRegs + (i * NT + nt) * 4 + x) * 32 + lane;
+          ll += v.y * f;
+          y0 = fmaf(src[0], fo, y0);
+          y1 = fmaf(src[64], fo, y1);
+        }
+        const int d = i / (C::kBox / 16) * C::kBox + g * (C::kBox / 8) + 2 * (i % (C::kBox / 16));
+        if (whole) {
+          if (r >= p.n_rows) continue;
+          const int h = hk * p.group + r / p.n_q, tq = r % p.n_q;
+          const float inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);  // (a NaN stays one)
+          *reinterpret_cast<uint32_t*>(p.o + (((int64_t)b * p.n_q + tq) * p.H + h) * D + d) = pack_bf16(y0 * inv, y1 * inv);
+          if (i == 0 && g == 0) {
+            p.lse[((int64_t)b * p.H + h) * p.n_q + tq] = (mm + log2f(ll)) * kLn2;
+            if (p.accumulate) p.whole_ml[(int64_t)bh * p.n_rows_pad + r] = make_float2(mm, ll);
           }
+        } else {
+          *reinterpret_cast<float2*>(p.part_o + (part + r) * D + d) = make_float2(y0, y1);
+          if (i == 0 && g == 0) p.part_ml[part + r] = make_float2(mm, ll);
+        }
       }
       }
       if (sg + 1 < n_seg) store_q();  // (every warp is done with the old rows)
