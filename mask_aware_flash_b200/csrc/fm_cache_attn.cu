@@ -155,6 +155,16 @@ __device__ __forceinline__ int units_per_run(const CacheAttnParams& p, int total
   return max((total + p.n_work - 1) / p.n_work, p.run_min);
 }
 
+// How many of the rows [i0, i1) see the key: those not before its pos (causal), less the union of its two stretches.
+__device__ __forceinline__ int rows_seen(const CacheAttnParams& p, const KeyBounds& k, int i0, int i1) {
+  if (p.causal) i0 = max(i0, k.j);
+  if (!k.in || i0 >= i1) return 0;
+  const int a0 = min(max(k.lts, i0), i1), a1 = max(min(k.lte, i1), a0);
+  const int b0 = min(max(k.uts, i0), i1), b1 = max(min(k.ute, i1), b0);
+  const int both = max(min(a1, b1) - max(a0, b0), 0);
+  return (i1 - i0) - (a1 - a0) - (b1 - b0) + both;
+}
+
 // The lists of units: list e is chunk e % n_chunk of (sequence, head) e / n_chunk.
 __device__ __forceinline__ int list_len(const CacheAttnParams& p, int e) {
   if (p.masked) return __ldcg(p.chunk_n + e);
@@ -212,16 +222,14 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const CacheAtt
       for (int x = 0; x < kGang; ++x)
 #pragma unroll
         for (int i = 0; i < 2; ++i) load_vectors(p, k[x][i], head + hg);
-#pragma unroll 1
-      for (int tq = 0; tq < p.n_q; ++tq)
 #pragma unroll
-        for (int x = 0; x < kGang; ++x)
+      for (int x = 0; x < kGang; ++x)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const bool s = key_seen(p, k[x][i], row0 + tq);
-            any[x] |= s;
-            all[x] &= s;
-          }
+        for (int i = 0; i < 2; ++i) {
+          const int seen = rows_seen(p, k[x][i], row0, row0 + p.n_q);
+          any[x] |= seen > 0;
+          all[x] &= seen == p.n_q;
+        }
     }
 #pragma unroll
     for (int x = 0; x < kGang; ++x) {
@@ -282,7 +290,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
   int* red = reinterpret_cast<int*>(smem + C::kRed);
   int* before = reinterpret_cast<int*>(smem + C::kBefore);
   const uint32_t ring = smem_u32(smem + C::kRing) + warp * kSlots * C::kSlotBytes;
-  const uint8_t* ring_p = smem + C::kRing + warp * kSlots * C::kSlotBytes;
+  uint8_t* ring_p = smem + C::kRing + warp * kSlots * C::kSlotBytes;
   const uint32_t bar0 = smem_u32(smem + C::kBar) + warp * kSlots * 8;
 
   if (threadIdx.x == 0) {
@@ -682,8 +690,17 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
         // ------------------------------------------------------------ O^T += V^T P^T
         wait();
         {
-          const uint8_t* vb = ring_p + (item + done) % kSlots * C::kSlotBytes;
+          uint8_t* vb = ring_p + (item + done) % kSlots * C::kSlotBytes;
           const int valid = missing ? 0 : len - slot0;
+          if (partial && valid < kPage) {  // slots never written may hold any bytes, a NaN's among them
+            for (int x = lane; x < (kPage - valid) * (D / 16); x += 32) {
+              const int row = valid + x / (D / 16), piece = x % (D / 16);
+              *reinterpret_cast<uint4*>(vb + piece / (C::kBox / 16) * kPage * C::kBox + row * C::kBox + piece % (C::kBox / 16) * 16) =
+                  make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();  // (the slot's next copy comes after these)
+            __syncwarp();
+          }
           constexpr int kWords = C::kBox / 32;  // 32-bit words of a row's piece that belongs to lane group g
 #pragma unroll
           for (int x = 0; x < C::kBoxes; ++x)
@@ -703,10 +720,6 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
                   const uint2 v = *reinterpret_cast<const uint2*>(vb + key * 64 + (((g >> 1) ^ ((key >> 1) & 3)) << 4) + (g & 1) * 8);
                   raw[r][0] = v.x;
                   raw[r][1] = v.y;
-                }
-                if (partial && key >= valid) {  // slots never written may hold any bytes, a NaN's among them
-#pragma unroll
-                  for (int w = 0; w < kWords; ++w) raw[r][w] = 0;
                 }
               }
 #pragma unroll
