@@ -806,7 +806,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
 // Last kernel (it may be resident before the one before ends, so what that wrote is read through L2).  The first CTAs join
 // the rows of the (sequence, head)s that several runs share, a CTA per row; the others add the softmax weights of kWeightSlots keys each to the cache's, from the stored scores.
 constexpr int kJoinThreads = 128;
-constexpr int kWeightSlots = 2048;
+constexpr int kWeightSlots = 512;
 constexpr int kMaxRows = 1024;
 
 struct Span {  // the runs that hold a (sequence, head), and where their partial sums are
@@ -827,15 +827,17 @@ __device__ __forceinline__ int64_t part_of(const CacheAttnParams& p, const Span&
 }
 // Maximum and sum of row r over its runs, by a warp (the same order for every caller).
 __device__ __forceinline__ float2 join_ml(const CacheAttnParams& p, const Span& s, int r, int lane) {
-  float m = kNegInf;
-  for (int c = s.first + lane; c <= s.last; c += 32) m = fmaxf(m, __ldcg(&p.part_ml[part_of(p, s, c) + r].x));
+  float2 v = make_float2(kNegInf, 0.f);  // of run first + lane
+  if (s.first + lane <= s.last) v = __ldcg(&p.part_ml[part_of(p, s, s.first + lane) + r]);
+  float m = v.x;
+  for (int c = s.first + lane + 32; c <= s.last; c += 32) m = fmaxf(m, __ldcg(&p.part_ml[part_of(p, s, c) + r].x));
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
   const float use = m == kNegInf ? 0.f : m;
-  float l = 0.f;
-  for (int c = s.first + lane; c <= s.last; c += 32) {
-    const float2 v = __ldcg(&p.part_ml[part_of(p, s, c) + r]);
-    l += v.y * ex2(v.x - use);
+  float l = v.y * ex2(v.x - use);
+  for (int c = s.first + lane + 32; c <= s.last; c += 32) {
+    const float2 w = __ldcg(&p.part_ml[part_of(p, s, c) + r]);
+    l += w.y * ex2(w.x - use);
   }
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
@@ -890,51 +892,53 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const CacheAtt
     if (threadIdx.x == 0) p.lse[((int64_t)b * p.H + h) * p.n_q + tq] = t.y == 0.f ? kNegInf : (t.x + log2f(t.y)) * kLn2;
     return;
   }
+  // Weights.  Four keys a thread; what does not depend on anything is loaded first, so that there are two memory latencies
+  // on the way, not one for each of length, runs, sums, liveness, scores.
+  constexpr int kKeys = kWeightSlots / kJoinThreads;
   const int cap = p.max_pages * kPage, per_bh = (cap + kWeightSlots - 1) / kWeightSlots;
   const int w = blockIdx.x - n_join, bh = w / per_bh, s0 = w % per_bh * kWeightSlots, b = bh / p.H_kv;
   const int len = min(max(__ldg(p.len + b), 0), cap);
-  if (s0 >= len) return;
   const Span s = span_of(p, bh);
+  float* weight = p.weight + (int64_t)bh * cap;
+  float x[kKeys];
+  uint8_t live[kKeys];
+#pragma unroll
+  for (int i = 0; i < kKeys; ++i) {
+    const int slot = s0 + i * kJoinThreads + threadIdx.x;
+    live[i] = slot < cap ? __ldcg(p.live + (int64_t)bh * p.max_pages + slot / kPage) : 0;
+    x[i] = slot < cap ? weight[slot] : 0.f;
+  }
+  if (s0 >= len) return;
+  const float4* sc = reinterpret_cast<const float4*>(p.score + ((int64_t)bh * cap + s0 + threadIdx.x) * p.rows4);
+  float4 v[kKeys];
+#pragma unroll
+  for (int i = 0; i < kKeys; ++i) {
+    live[i] = live[i] && s0 + i * kJoinThreads + (int)threadIdx.x < len;
+    v[i] = live[i] ? __ldcg(sc + i * kJoinThreads * p.rows4 / 4) : make_float4(kNegInf, kNegInf, kNegInf, kNegInf);
+  }
   for (int r = warp; r < p.rows4; r += kJoinThreads / 32) {
     float2 t = make_float2(kNegInf, 0.f);
     if (r < p.n_rows) t = s.first == s.last ? __ldcg(&p.whole_ml[(int64_t)bh * p.n_rows_pad + r]) : join_ml(p, s, r, lane);
     if (lane == 0) ml[r] = make_float2(t.x == kNegInf ? 0.f : t.x, t.y > 0.f ? 1.f / t.y : (t.y == 0.f ? 0.f : t.y));
   }
   __syncthreads();
-  // four keys a thread, their loads in flight together
-  constexpr int kKeys = 4;
 #pragma unroll 1
-  for (int s1 = s0; s1 < min(s0 + kWeightSlots, len); s1 += kKeys * kJoinThreads) {
-    float x[kKeys];
-    bool live[kKeys];
+  for (int r = 0; r < p.rows4; r += 4) {
+    const float2 m0 = ml[r], m1 = ml[r + 1], m2 = ml[r + 2], m3 = ml[r + 3];
 #pragma unroll
     for (int i = 0; i < kKeys; ++i) {
-      const int slot = s1 + i * kJoinThreads + threadIdx.x;
-      live[i] = slot < len && __ldcg(p.live + (int64_t)bh * p.max_pages + slot / kPage);
-      x[i] = live[i] ? p.weight[(int64_t)bh * cap + slot] : 0.f;
+      float y = ex2(v[i].x - m0.x) * m0.y;
+      // rows behind the last one hold no score
+      if (r + 1 < p.n_rows) y += ex2(v[i].y - m1.x) * m1.y;
+      if (r + 2 < p.n_rows) y += ex2(v[i].z - m2.x) * m2.y;
+      if (r + 3 < p.n_rows) y += ex2(v[i].w - m3.x) * m3.y;
+      x[i] += y;
+      if (r + 4 < p.rows4 && live[i]) v[i] = __ldcg(sc + (i * kJoinThreads * p.rows4 + r + 4) / 4);
     }
-    const float4* sc = reinterpret_cast<const float4*>(p.score + ((int64_t)bh * cap + s1 + threadIdx.x) * p.rows4);
-#pragma unroll 1
-    for (int r = 0; r < p.rows4; r += 4) {
-      float4 v[kKeys];
-#pragma unroll
-      for (int i = 0; i < kKeys; ++i)
-        v[i] = live[i] ? __ldcg(sc + (i * kJoinThreads * p.rows4 + r) / 4) : make_float4(kNegInf, kNegInf, kNegInf, kNegInf);
-      const float2 m0 = ml[r], m1 = ml[r + 1], m2 = ml[r + 2], m3 = ml[r + 3];
-#pragma unroll
-      for (int i = 0; i < kKeys; ++i) {
-        float y = ex2(v[i].x - m0.x) * m0.y;
-        // rows behind the last one hold no score
-        if (r + 1 < p.n_rows) y += ex2(v[i].y - m1.x) * m1.y;
-        if (r + 2 < p.n_rows) y += ex2(v[i].z - m2.x) * m2.y;
-        if (r + 3 < p.n_rows) y += ex2(v[i].w - m3.x) * m3.y;
-        x[i] += y;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kKeys; ++i)
-      if (live[i]) p.weight[(int64_t)bh * cap + s1 + i * kJoinThreads + threadIdx.x] = x[i];
   }
+#pragma unroll
+  for (int i = 0; i < kKeys; ++i)
+    if (live[i]) weight[s0 + i * kJoinThreads + threadIdx.x] = x[i];
 }
 
 // ------------------------------------------------------------------------------------------- host
