@@ -51,13 +51,13 @@ struct KeyWeightSmem {
   static constexpr int kStages = D == 256 ? 2 : D == 128 ? 4 : 8;  // query tiles in flight
   static constexpr int kK = 0;
   static constexpr int kQ = kK + kKBufs * kTileBytes;
-  static constexpr int kLse = kQ + kStages * kTileBytes;     // [warpgroups][2][128] -log2 LSE
-  static constexpr int kSum = kLse + kGroups * 2 * kTile * 4;  // [2][warpgroups - 1][128] sums; [0][0]: of the CTA
+  static constexpr int kLse = kQ + kStages * kTileBytes;     // [warps of sums][128] -log2 LSE
+  static constexpr int kSum = kLse + kGroups * 4 * kTile * 4;  // [2][warpgroups - 1][128] sums; [0][0]: of the CTA
   static constexpr int kItems = kSum + 2 * (kGroups - 1) * kTile * 4;  // int4 [readers][kRing]: listed items
   static constexpr int kBar = kItems + kReaders * kRing * 16;
   enum { K_FULL, K_EMPTY = K_FULL + kKBufs, Q_FULL = K_EMPTY + kKBufs, Q_EMPTY = Q_FULL + kStages,
          S_FULL = Q_EMPTY + kStages, S_EMPTY = S_FULL + kBufs, ITEM = S_EMPTY + kBufs, ITEM_FREE = ITEM + kReaders * kRing,
-         LSE_FULL = ITEM_FREE + kReaders * kRing, SUM_FULL = LSE_FULL + 2 * kGroups, SUM_EMPTY = SUM_FULL + 2, DRAIN = SUM_EMPTY + 2, kNumBars };
+         SUM_FULL = ITEM_FREE + kReaders * kRing, SUM_EMPTY = SUM_FULL + 2, DRAIN = SUM_EMPTY + 2, kNumBars };
   static constexpr int kMisc = kBar + kNumBars * 8;  // [0] TMEM base, [1] abort flag, [2] zero
   static constexpr int kBytes = kMisc + 16;
   static constexpr int kAlloc = kBytes + 1024;
@@ -118,39 +118,26 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) { 
   return v;
 }
 
-// 16 columns of this thread's TMEM lane: the load, and the wait for every load so far (which the registers are tied to, so
-// that none of them is read before it).
-__device__ __forceinline__ void tmem_ld16_start(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_ld16_end(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
-}
-
-// Adds the weights of 16 scores to the four running sums; bit i of `masked`: query i does not see the key.  nl: -LSE of the
-// queries in log2 units.  (One score an instruction: packed pairs would halve the multiply-adds and additions, but cost
-// more register moves than that.)
-__device__ __forceinline__ void add_block(const uint32_t (&s)[16], const float* nl, float scale, uint32_t masked, float (&acc)[4]) {
-  float w[16];
+// Adds the weights of 32 scores to the four running sums; bit i of `masked` (only of a partial tile): query i does not see
+// the key.  nl: -LSE of the queries in log2 units.  (One score an instruction: packed pairs would halve the multiply-adds and
+// additions, but cost more register moves than that.)
+__device__ __forceinline__ void add_block(const uint32_t (&s)[32], const float* nl, float scale, bool partial, uint32_t masked,
+                                          float (&acc)[4]) {
+  float w[32];
 #pragma unroll
-  for (int c = 0; c < 16; c += 4) {
+  for (int c = 0; c < 32; c += 4) {
     const float4 v = *reinterpret_cast<const float4*>(nl + c);
     w[c] = ex2(fmaf(__uint_as_float(s[c]), scale, v.x));
     w[c + 1] = ex2(fmaf(__uint_as_float(s[c + 1]), scale, v.y));
     w[c + 2] = ex2(fmaf(__uint_as_float(s[c + 2]), scale, v.z));
     w[c + 3] = ex2(fmaf(__uint_as_float(s[c + 3]), scale, v.w));
   }
-  if (__any_sync(0xffffffffu, masked != 0u)) {
+  if (partial) {
 #pragma unroll
-    for (int c = 0; c < 16; ++c) w[c] = ((masked >> c) & 1u) ? 0.f : w[c];
+    for (int c = 0; c < 32; ++c) w[c] = ((masked >> c) & 1u) ? 0.f : w[c];
   }
 #pragma unroll
-  for (int c = 0; c < 16; ++c) acc[c & 3] += w[c];
+  for (int c = 0; c < 32; ++c) acc[c & 3] += w[c];
 }
 
 // The key tile and head of piece of work `w`: groups of heads, in each the key tiles by rank (longest lists first).
@@ -189,7 +176,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < S::kNumBars; ++i) mbar_init(bar(i), 1);
     for (int i = 0; i < kBufs; ++i) mbar_init(bar(S::S_EMPTY + i), kTile);
     for (int i = 0; i < kGroups * kRing; ++i) mbar_init(bar(S::ITEM_FREE + i), 4);  // a warpgroup's warps
-    for (int i = 0; i < 2 * kGroups; ++i) mbar_init(bar(S::LSE_FULL + i), 4);  // a warpgroup's warps
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(S::SUM_FULL + i), 4 * (kGroups - 1));
       mbar_init(bar(S::SUM_EMPTY + i), 4);
@@ -213,23 +199,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kListWarp) {
     // ------------------------------------------------------------ list role
-    // The whole warp reads the lists (32 entries at a time: an entry's latency would otherwise pace the kernel), lane 0
-    // hands the items out.
+    // The whole warp reads the lists (32 entries at a time) and hands out eight items at a time, a lane each: this warp shares
+    // its scheduler with four busy ones, and one thread's instructions per item would pace the kernel.
     int qi = 0;  // query tiles so far
-    int pushed[kReaders];
+    int pushed[kGroups];  // items of each warpgroup's ring so far (the other two rings: qi)
 #pragma unroll
-    for (int i = 0; i < kReaders; ++i) pushed[i] = 0;
+    for (int i = 0; i < kGroups; ++i) pushed[i] = 0;
     bool ok = true;
-    auto push = [&](int reader, int& n, const int4& e) {
-      if (lane == 0) {
-        const int at = reader * kRing + n % kRing;
-        ok = ok && (n < kRing || mbar_wait_idle(bar(S::ITEM_FREE + at), (n / kRing - 1) & 1, abort_flag));
-        if (ok) {
-          items[at] = e;
-          mbar_arrive(bar(S::ITEM + at));
-        }
+    // puts `e` into place n of a reader's ring, by the calling lane
+    auto put = [&](int reader, int n, const int4& e) {
+      const int at = reader * kRing + n % kRing;
+      ok = ok && (n < kRing || mbar_wait_idle(bar(S::ITEM_FREE + at), (n / kRing - 1) & 1, abort_flag));
+      if (ok) {
+        items[at] = e;
+        mbar_arrive(bar(S::ITEM + at));
       }
-      ++n;
     };
     int bh = 0, kt = 0;
     if (work0 < p.n_work) work_of(p, work0, bh, kt);
@@ -251,7 +235,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n_items = total > rank ? (total - rank + step - 1) / step : 0;  // of this CTA
 #pragma unroll
       for (int g = 0; g < kGroups; ++g)
-        if ((g - qi % kGroups + kGroups) % kGroups >= n_items) push(g, pushed[g], make_int4(0, kLast | kEmpty, kt, b_hk));
+        if ((g - qi % kGroups + kGroups) % kGroups >= n_items) {
+          if (lane == 0) put(g, pushed[g], make_int4(0, kLast | kEmpty, kt, b_hk));
+          ++pushed[g];
+        }
       int item = 0, skip = rank;  // items handed out; entries to pass over before the next one
       for (int hg = 0; hg < p.q_per_kv; ++hg) {
         const int n = __shfl_sync(0xffffffffu, hg < 32 ? n0 : n1, hg & 31);
@@ -260,15 +247,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (; at < n; at += 32 * step) {
           const int mine = at + lane * step < n ? __ldg(list + at + lane * step) : 0;
           const int here = min(32, (n - at + step - 1) / step);
-          for (int j = 0; j < here; ++j, ++item, ++qi) {
-            const int entry = __shfl_sync(0xffffffffu, mine, j);
-            const int4 e = make_int4(entry, hg | (item == 0 ? kFirst : 0) | (item + 1 == n_items ? kLast : 0), kt, b_hk);
-            push(kGroups, pushed[kGroups], e);
-            push(kGroups + 1, pushed[kGroups + 1], e);
+          for (int j0 = 0; j0 < here; j0 += 8) {
+            const int n_now = min(8, here - j0), entry = __shfl_sync(0xffffffffu, mine, j0 + (lane & 7));
+            if (lane < n_now) {
+              const int q = qi + lane, reader = q % kGroups, i = item + lane;
+              const int4 e = make_int4(entry, hg | (i == 0 ? kFirst : 0) | (i + 1 == n_items ? kLast : 0), kt, b_hk);
+              put(kGroups, q, e);
+              put(kGroups + 1, q, e);
+              int n_before = pushed[0];
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g)
-              if (qi % kGroups == g) push(g, pushed[g], make_int4(entry, hg | (item + kGroups >= n_items ? kLast : 0), kt, b_hk));
-            ok = __shfl_sync(0xffffffffu, ok, 0);
+              for (int g = 1; g < kGroups; ++g) n_before = reader == g ? pushed[g] : n_before;
+              put(reader, n_before + lane / kGroups, make_int4(entry, hg | (i + kGroups >= n_items ? kLast : 0), kt, b_hk));
+            }
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+              const int first = (g - qi % kGroups + kGroups) % kGroups;  // this warpgroup's first item of the eight
+              pushed[g] += first < n_now ? (n_now - 1 - first) / kGroups + 1 : 0;
+            }
+            item += n_now;
+            qi += n_now;
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
           }
           if (!ok) break;
@@ -280,10 +278,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       bh = bh_next;
       kt = kt_next;
       w = w_next;
-      ok = __shfl_sync(0xffffffffu, ok, 0);  // (the lanes leave the loop together)
+      ok = __all_sync(0xffffffffu, ok);  // (the lanes leave the loop together)
     }
+    if (lane == 0) {
 #pragma unroll
-    for (int i = 0; i < kReaders; ++i) push(i, pushed[i], make_int4(0, kEnd, 0, 0));
+      for (int i = 0; i < kGroups; ++i) put(i, pushed[i], make_int4(0, kEnd, 0, 0));
+      put(kGroups, qi, make_int4(0, kEnd, 0, 0));
+      put(kGroups + 1, qi, make_int4(0, kEnd, 0, 0));
+    }
     if (!ok && lane == 0) record_failure(p.status, abort_flag, 61);
   } else if (warp == kLoadWarp) {
     // ------------------------------------------------------------ load role
@@ -373,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------- exponentials and sums: one key per thread
     const int wg = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
-    float* my_lse = lse_s + wg * 2 * kTile;
+    float* nl = lse_s + warp * kTile;  // (each warp has its own: no barrier between the warps for it)
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     int ends = 0;
     bool ok = true;
@@ -389,10 +391,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (step == 1 && key_at >= 0) p.weight[key_at] = p.accumulate ? p.weight[key_at] + sum : sum;
     };
     int mine = 0;  // query tiles so far
-    // LSE of this thread's row of an item's query tile; -inf past n_q (and for rows that see no key): their p is 0
+    // LSE of four rows of an item's query tile (lane, lane + 32, ..); -inf past n_q (and for rows that see no key): their p is 0
     auto load_lse = [&](const int4& e) {
-      const int row = (e.x >> 1) * kTile + r, h = (e.w & 0xFFFF) * p.q_per_kv + (e.y & 255);
-      return row < p.n_q && !(e.y & (kEmpty | kEnd)) ? __ldg(p.lse + ((int64_t)((uint32_t)e.w >> 16) * p.H + h) * p.n_q + row) : kNegInf;
+      const int row = (e.x >> 1) * kTile + lane, h = (e.w & 0xFFFF) * p.q_per_kv + (e.y & 255);
+      const float* src = p.lse + ((int64_t)((uint32_t)e.w >> 16) * p.H + h) * p.n_q + row;
+      const int n = e.y & (kEmpty | kEnd) ? 0 : p.n_q - row;
+      return make_float4(n > 0 ? __ldg(src) : kNegInf, n > 32 ? __ldg(src + 32) : kNegInf, n > 64 ? __ldg(src + 64) : kNegInf,
+                         n > 96 ? __ldg(src + 96) : kNegInf);
     };
     // bounds of this thread's key for an item: lts, lte, uts, ute
     auto load_bounds = [&](const int4& e) {
@@ -408,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return v;
     };
     int4 e_next, bounds_next;
-    float x_next = 0.f;
+    float4 x_next;
     bool have_next = false;
     for (int it = 0; ok; ++it) {
       auto take = [&](int i) {  // reads a listed item and gives its place back
@@ -419,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return v;
       };
       int4 e, bounds;
-      float x;
+      float4 x;
       if (have_next) {
         e = e_next;
         x = x_next;
@@ -432,12 +437,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         bounds = load_bounds(e);
       }
       if (e.y & kEnd) break;
-      const int b = (int)((uint32_t)e.w >> 16), hk = e.w & 0xFFFF, key = e.z * kTile + r, lb = mine & 1;
-      if (!(e.y & kEmpty)) {
-        my_lse[lb * kTile + r] = x == kNegInf ? kNegInf : -x * 1.4426950408889634f;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(S::LSE_FULL + 2 * wg + lb));
-      }
+      const int b = (int)((uint32_t)e.w >> 16), hk = e.w & 0xFFFF, key = e.z * kTile + r;
+      auto log2_neg = [](float v) { return v == kNegInf ? kNegInf : -v * 1.4426950408889634f; };
+      __syncwarp();  // (the last item's have been read)
+      nl[lane] = log2_neg(x.x);
+      nl[lane + 32] = log2_neg(x.y);
+      nl[lane + 64] = log2_neg(x.z);
+      nl[lane + 96] = log2_neg(x.w);
+      __syncwarp();
       // the next item, if it is listed already: its LSE and bounds are in flight during this one's exponentials
       have_next = __all_sync(0xffffffffu, mbar_test(bar(S::ITEM + wg * kRing + (it + 1) % kRing), ((it + 1) / kRing) & 1));
       if (have_next) {
@@ -448,35 +455,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(e.y & kEmpty)) {
         const int q0 = (e.x >> 1) * kTile;
         const bool ragged = q0 + kTile > p.n_q, partial = (e.x & 1) || ragged;
-        // the values are there (and those of the item before last have been read)
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(S::LSE_FULL + 2 * wg + lb), (mine >> 1) & 1, abort_flag));
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(S::S_FULL + wg), mine & 1, abort_flag)) && ok;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(S::S_FULL + wg), mine & 1, abort_flag));
         if (!ok) break;
-        const float* nl = my_lse + lb * kTile;
         auto mask_word = [&](int jb) {  // bit i: query q0 + 32 jb + i does not see this key
           const int base = q0 + jb * 32;
           const uint32_t mw = interval_bits32(bounds.x, bounds.y, base) | interval_bits32(bounds.z, bounds.w, base);
           return !ragged || base + 32 <= p.n_q ? mw : mw | (base >= p.n_q ? 0xFFFFFFFFu : 0xFFFFFFFFu << (p.n_q - base));
         };
         tc_fence_after();
-        // 16 scores at a time, the next 16 in flight
-        uint32_t s0[16], s1[16];
+        // (not unrolled: the code of one block stays in the instruction cache)
         const uint32_t t0 = tmem + wg * 128 + lane_addr;
-        tmem_ld16_start(t0, s0);
-#pragma unroll 1  // (the code of two blocks stays in the instruction cache)
+#pragma unroll 1
         for (int jb = 0; jb < 4; ++jb) {
-          const uint32_t masked = partial ? mask_word(jb) : 0u;
-          tmem_ld16_end(s0);
-          tmem_ld16_start(t0 + jb * 32 + 16, s1);
-          add_block(s0, nl + jb * 32, p.scale_log2, masked & 0xFFFFu, acc);
-          tmem_ld16_end(s1);
-          if (jb < 3) {
-            tmem_ld16_start(t0 + jb * 32 + 32, s0);
-          } else {
+          uint32_t s[32];
+          tmem_ld32(t0 + jb * 32, s);
+          if (jb == 3) {
             tc_fence_before();
             mbar_arrive(bar(S::S_EMPTY + wg));
           }
-          add_block(s1, nl + jb * 32 + 16, p.scale_log2, masked >> 16, acc);
+          add_block(s, nl + jb * 32, p.scale_log2, partial, partial ? mask_word(jb) : 0u, acc);
         }
         ++mine;
       }
