@@ -450,7 +450,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (have_next) {
         e_next = take(it + 1);
         x_next = load_lse(e_next);
-        bounds_next = load_bounds(e_next);
+        // (the bounds stay while the key tile and the mask do)
+        const bool same = e_next.z == e.z && e_next.w == e.w && !(e.y & kEmpty) && (p.Hm == 1 || ((e_next.y ^ e.y) & 255) == 0);
+        bounds_next = bounds;
+        if (!same) bounds_next = load_bounds(e_next);
       }
       if (!(e.y & kEmpty)) {
         const int q0 = (e.x >> 1) * kTile;
