@@ -65,8 +65,8 @@ template <>
 struct Raw16<__nv_bfloat16> {
   uint4 v[2];
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    v[0] = __ldg(reinterpret_cast<const uint4*>(p));
-    v[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    v[0] = *(reinterpret_cast<const uint4*>(p));
+    v[1] = *(reinterpret_cast<const uint4*>(p) + 1);
   }
   // bit pattern (as fp32) of the largest |x|: both halves of a word at once
   __device__ __forceinline__ uint32_t max_bits() const {
@@ -97,7 +97,7 @@ struct Raw16<float> {
   float4 v[4];
   __device__ __forceinline__ void load(const float* p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __ldg(reinterpret_cast<const float4*>(p) + i);
+    for (int i = 0; i < 4; ++i) v[i] = *(reinterpret_cast<const float4*>(p) + i);
   }
   __device__ __forceinline__ uint32_t max_bits() const {
     float x[16];
@@ -146,14 +146,16 @@ template <int D, typename T, bool E4M3>
 __global__ void __launch_bounds__(2 * D) append_kernel(const AppendParams p) {
   constexpr int kThreads = 2 * D, kPieces = D / 16;
   __shared__ uint32_t red[2][kThreads / 32];
+  grid_wait();
+  grid_launch_next();
   const int which = blockIdx.x & 1, hk = blockIdx.y, b = blockIdx.z;
-  const int start = __ldg(p.start + b);
-  const int count = p.count ? min(max(__ldg(p.count + b), 0), p.n_new) : p.n_new;
+  const int start = *(p.start + b);
+  const int count = p.count ? min(max(*(p.count + b), 0), p.n_new) : p.n_new;
   const int block = (start >> 6) + (int)(blockIdx.x >> 1);
   if (block < 0 || block >= p.max_pages) return;
   const int64_t t0 = (int64_t)block * kPage - start;  // token of the block's first slot (negative: older slots)
   if (t0 >= count || t0 + kPage <= 0) return;
-  const int page = __ldg(p.page_table + (int64_t)b * p.max_pages + block);
+  const int page = *(p.page_table + (int64_t)b * p.max_pages + block);
   Raw16<T> x[2];
   bool fresh[2];
   uint32_t bits = 0;
@@ -208,21 +210,22 @@ __global__ void __launch_bounds__(2 * D) append_kernel(const AppendParams p) {
     if (t >= 0 && t < count) {
       const int64_t slot = ((int64_t)b * p.H_kv + hk) * p.max_pages * kPage + (int64_t)block * kPage + threadIdx.x;
       if (p.weight) p.weight[slot] = 0.f;
-      if (p.pos) p.pos[slot] = (p.row ? __ldg(p.row + b) : start) + (int)t;
+      if (p.pos) p.pos[slot] = (p.row ? *(p.row + b) : start) + (int)t;
     }
   }
 }
 
 template <int D>
-void launch_append(const AppendParams& p, int B, int dtype, int code_type, cudaStream_t s) {
+cudaError_t launch_append(const AppendParams& p, int B, int dtype, int code_type, cudaStream_t s) {
+  EarlyLaunch launch(s);
   // a run of n tokens touches at most ceil((63 + n) / 64) blocks
-  const dim3 grid(2 * (unsigned)(((int64_t)p.n_new + kPage - 1 + kPage - 1) / kPage), p.H_kv, B);
+  launch.cfg.gridDim = dim3(2 * (unsigned)(((int64_t)p.n_new + kPage - 1 + kPage - 1) / kPage), p.H_kv, B);
+  launch.cfg.blockDim = dim3(2 * D);
   if (dtype == 0)
-    code_type ? append_kernel<D, __nv_bfloat16, true><<<grid, 2 * D, 0, s>>>(p)
-              : append_kernel<D, __nv_bfloat16, false><<<grid, 2 * D, 0, s>>>(p);
-  else
-    code_type ? append_kernel<D, float, true><<<grid, 2 * D, 0, s>>>(p)
-              : append_kernel<D, float, false><<<grid, 2 * D, 0, s>>>(p);
+    return code_type ? cudaLaunchKernelEx(&launch.cfg, append_kernel<D, __nv_bfloat16, true>, p)
+                     : cudaLaunchKernelEx(&launch.cfg, append_kernel<D, __nv_bfloat16, false>, p);
+  return code_type ? cudaLaunchKernelEx(&launch.cfg, append_kernel<D, float, true>, p)
+                   : cudaLaunchKernelEx(&launch.cfg, append_kernel<D, float, false>, p);
 }
 
 // ------------------------------------------------------------------------------------------- evict
@@ -317,11 +320,13 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
   constexpr int kSelWarps = kSelThreads / 32;
   extern __shared__ uint32_t keys[];
   __shared__ __align__(16) SelSmem sm;
+  grid_wait();
+  grid_launch_next();
   const int rank = (int)cluster_rank(), size = (int)cluster_size();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int hk = blockIdx.y, b = blockIdx.z;
   const int64_t bh = (int64_t)b * p.H_kv + hk;
-  const int n = min(max(__ldg(p.len + b), 0), p.src_max * kPage);
+  const int n = min(max(*(p.len + b), 0), p.src_max * kPage);
   if (threadIdx.x == 0 && rank == 0) p.n_kept[bh] = min(n, p.budget);
   int32_t* kept = p.kept + bh * p.budget;
   const float* w = p.src_weight + bh * p.src_max * kPage;
@@ -339,9 +344,9 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
       for (int u = 0; u < 4; ++u) f[u] = to + u * step < end ? from(to + u * step) : -1;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        page[u] = f[u] >= 0 ? __ldg(table + f[u] / kPage) : -1;
-        x[u] = to_w && f[u] >= 0 ? __ldg(w + f[u]) : 0.f;
-        q[u] = to_pos && pos && f[u] >= 0 ? __ldg(pos + f[u]) : f[u];
+        page[u] = f[u] >= 0 ? *(table + f[u] / kPage) : -1;
+        x[u] = to_w && f[u] >= 0 ? *(w + f[u]) : 0.f;
+        q[u] = to_pos && pos && f[u] >= 0 ? *(pos + f[u]) : f[u];
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u)
@@ -362,14 +367,14 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
   // this CTA's run of slots; a length below the table's leaves CTAs fewer slots, not other ones without any
   const int run = min(p.chunk, (((older + size - 1) / size) + 31) / 32 * 32);
   const int i0 = min(rank * run, older), mine = min(i0 + run, older) - i0;
-  auto key = [&](int i) { return kHeld ? keys[i] : weight_key(__ldg(w + i0 + i)); };
+  auto key = [&](int i) { return kHeld ? keys[i] : weight_key(*(w + i0 + i)); };
   // The range of the keys: digits are taken of key - lowest, from the highest bit that occurs, so that a pass tells as many
   // keys apart as its bins can (of weights within a few octaves, the top bits of the key itself would fill a few bins).
   uint32_t lowest = 0xFFFFFFFFu, highest = 0;
   for (int i = threadIdx.x; i < mine; i += 8 * kSelThreads) {
     float x[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) x[u] = i + u * kSelThreads < mine ? __ldg(w + i0 + i + u * kSelThreads) : 0.f;
+    for (int u = 0; u < 8; ++u) x[u] = i + u * kSelThreads < mine ? *(w + i0 + i + u * kSelThreads) : 0.f;
 #pragma unroll
     for (int u = 0; u < 8; ++u)
       if (i + u * kSelThreads < mine) {
@@ -564,15 +569,17 @@ template <int D, bool E4M3>
 __global__ void __launch_bounds__(2 * D, 1024 / (2 * D)) compact_kernel(const EvictParams p) {
   constexpr int kThreads = 2 * D, kPieces = D / 16;
   __shared__ uint32_t red[2][kThreads / 32];
+  grid_wait();
+  grid_launch_next();
   const int block = blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
   const int64_t bh = (int64_t)b * p.H_kv + hk;
-  const int n = __ldg(p.n_kept + bh);
-  const int page = __ldg(p.dst_table + (int64_t)b * p.dst_max + block);
+  const int n = __ldcg(p.n_kept + bh);
+  const int page = *(p.dst_table + (int64_t)b * p.dst_max + block);
   int row[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {  // (entries behind the n-th are there, without a meaning)
     const int to = block * kPage + (threadIdx.x + i * kThreads) / kPieces;
-    row[i] = to < p.budget ? __ldg(p.kept + bh * p.budget + to) : -1;
+    row[i] = to < p.budget ? __ldcg(p.kept + bh * p.budget + to) : -1;
   }
   if (block == 0 && hk == 0 && threadIdx.x == 0) p.new_len[b] = n;
   if (block * kPage >= n || page < 0 || page >= p.dst_pages) return;
@@ -588,8 +595,8 @@ __global__ void __launch_bounds__(2 * D, 1024 / (2 * D)) compact_kernel(const Ev
       scale[x][i] = 0.f;
       if (row[i] >= 0) {
         const int64_t at = (int64_t)(row[i] / kPage) * p.H_kv + hk;
-        scale[x][i] = __ldg(p.src_scale[x] + at);
-        raw[x][i] = __ldg(reinterpret_cast<const uint4*>(p.src_codes[x] + (at * kPage + row[i] % kPage) * D) + piece % kPieces);
+        scale[x][i] = *(p.src_scale[x] + at);
+        raw[x][i] = *(reinterpret_cast<const uint4*>(p.src_codes[x] + (at * kPage + row[i] % kPage) * D) + piece % kPieces);
       }
     }
   }
@@ -627,18 +634,11 @@ __global__ void __launch_bounds__(2 * D, 1024 / (2 * D)) compact_kernel(const Ev
 
 template <bool kHeld, int kThreads>
 cudaError_t launch_select(const EvictParams& p, int B, int cluster, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
+  EarlyLaunch launch(s, cluster);
+  cudaLaunchConfig_t& cfg = launch.cfg;
   cfg.gridDim = dim3(cluster, p.H_kv, B);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kHeld ? p.chunk * 4 : 0;
-  cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = cluster;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
   if (kHeld && !smem_opt_in<select_kernel<kHeld, kThreads>>(kSelMaxKeys * 4)) return cudaErrorInvalidValue;
   return cudaLaunchKernelEx(&cfg, select_kernel<kHeld, kThreads>, p);
 }
@@ -679,10 +679,10 @@ fm_status fm_cache_append(const fm_kv_cache* c, const void* k, const void* v, in
   p.n_pages = c->n_pages;
   p.max_pages = c->max_pages;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (c->D == 64) fm::launch_append<64>(p, c->B, dtype, c->code_type, s);
-  else if (c->D == 128) fm::launch_append<128>(p, c->B, dtype, c->code_type, s);
-  else fm::launch_append<256>(p, c->B, dtype, c->code_type, s);
-  return cudaGetLastError() == cudaSuccess ? FM_OK : FM_ERR_CUDA;
+  const cudaError_t e = c->D == 64    ? fm::launch_append<64>(p, c->B, dtype, c->code_type, s)
+                        : c->D == 128 ? fm::launch_append<128>(p, c->B, dtype, c->code_type, s)
+                                      : fm::launch_append<256>(p, c->B, dtype, c->code_type, s);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? FM_OK : FM_ERR_CUDA;
 }
 
 size_t fm_cache_evict_workspace_bytes(const fm_kv_cache* src, int32_t budget) {
@@ -740,17 +740,20 @@ fm_status fm_cache_evict(const fm_kv_cache* src, const fm_kv_cache* dst, const i
   const bool held = p.chunk <= fm::kSelMaxKeys;
   // 1024 threads a CTA where there is one CTA per SM at most, 512 where two share one
   const bool wide = lists * cluster <= 148;
-  const cudaError_t e = held ? (wide ? fm::launch_select<true, 1024>(p, src->B, cluster, s) : fm::launch_select<true, 512>(p, src->B, cluster, s))
-                             : fm::launch_select<false, 1024>(p, src->B, cluster, s);
+  cudaError_t e = held ? (wide ? fm::launch_select<true, 1024>(p, src->B, cluster, s) : fm::launch_select<true, 512>(p, src->B, cluster, s))
+                       : fm::launch_select<false, 1024>(p, src->B, cluster, s);
   if (e != cudaSuccess) return FM_ERR_CUDA;
-  const dim3 grid((unsigned)((budget + fm::kPage - 1) / fm::kPage), src->H_kv, src->B);
+  fm::EarlyLaunch launch(s);
+  cudaLaunchConfig_t& cfg = launch.cfg;
+  cfg.gridDim = dim3((unsigned)((budget + fm::kPage - 1) / fm::kPage), src->H_kv, src->B);
+  cfg.blockDim = dim3(2 * src->D);
   if (src->D == 64)
-    src->code_type ? fm::compact_kernel<64, true><<<grid, 128, 0, s>>>(p) : fm::compact_kernel<64, false><<<grid, 128, 0, s>>>(p);
+    e = src->code_type ? cudaLaunchKernelEx(&cfg, fm::compact_kernel<64, true>, p) : cudaLaunchKernelEx(&cfg, fm::compact_kernel<64, false>, p);
   else if (src->D == 128)
-    src->code_type ? fm::compact_kernel<128, true><<<grid, 256, 0, s>>>(p) : fm::compact_kernel<128, false><<<grid, 256, 0, s>>>(p);
+    e = src->code_type ? cudaLaunchKernelEx(&cfg, fm::compact_kernel<128, true>, p) : cudaLaunchKernelEx(&cfg, fm::compact_kernel<128, false>, p);
   else
-    src->code_type ? fm::compact_kernel<256, true><<<grid, 512, 0, s>>>(p) : fm::compact_kernel<256, false><<<grid, 512, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FM_OK : FM_ERR_CUDA;
+    e = src->code_type ? cudaLaunchKernelEx(&cfg, fm::compact_kernel<256, true>, p) : cudaLaunchKernelEx(&cfg, fm::compact_kernel<256, false>, p);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? FM_OK : FM_ERR_CUDA;
 }
 
 }  // extern "C"

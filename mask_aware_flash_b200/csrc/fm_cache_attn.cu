@@ -119,11 +119,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return r;
 }
 
-// Programmatic launches: a kernel of a call starts while the one before it in the stream ends, waits here for that one's
-// results, and lets the next one start.
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // Bounds of one cached key: its row index and its two masked stretches.
 struct KeyBounds {
   int j, lts, lte, uts, ute;
@@ -132,17 +127,17 @@ struct KeyBounds {
 __device__ __forceinline__ void load_pos(const CacheAttnParams& p, KeyBounds& k, int64_t bh, int slot, int len) {
   k.in = slot < len;
   k.j = slot;
-  if (k.in && p.pos) k.j = __ldg(p.pos + bh * p.max_pages * kPage + slot);
+  if (k.in && p.pos) k.j = *(p.pos + bh * p.max_pages * kPage + slot);
 }
 __device__ __forceinline__ void load_vectors(const CacheAttnParams& p, KeyBounds& k, int64_t bhm) {
   k.lts = k.lte = 0x7FFFFFFF;  // canonical empty stretches; also those of keys outside the vectors
   k.uts = k.ute = 0;
   if (k.in && k.j >= 0 && k.j < p.n_k) {
     const int64_t at = bhm * p.n_k + k.j;
-    if (p.vec[0]) k.lts = __ldg(p.vec[0] + at);
-    if (p.vec[1]) k.lte = __ldg(p.vec[1] + at);
-    if (p.vec[2]) k.uts = __ldg(p.vec[2] + at);
-    if (p.vec[3]) k.ute = __ldg(p.vec[3] + at);
+    if (p.vec[0]) k.lts = *(p.vec[0] + at);
+    if (p.vec[1]) k.lte = *(p.vec[1] + at);
+    if (p.vec[2]) k.uts = *(p.vec[2] + at);
+    if (p.vec[3]) k.ute = *(p.vec[3] + at);
   }
 }
 __device__ __forceinline__ bool key_seen(const CacheAttnParams& p, const KeyBounds& k, int i) {
@@ -168,7 +163,7 @@ __device__ __forceinline__ int rows_seen(const CacheAttnParams& p, const KeyBoun
 // The lists of units: list e is chunk e % n_chunk of (sequence, head) e / n_chunk.
 __device__ __forceinline__ int list_len(const CacheAttnParams& p, int e) {
   if (p.masked) return __ldcg(p.chunk_n + e);
-  return (min(max(__ldg(p.len + e / p.H_kv), 0), p.max_pages * kPage) + kPage - 1) / kPage;
+  return (min(max(*(p.len + e / p.H_kv), 0), p.max_pages * kPage) + kPage - 1) / kPage;
 }
 // List and place in it of unit u.  before[t]: units before list t * per.
 __device__ __forceinline__ int2 find_unit(const CacheAttnParams& p, const int* before, int threads, int per, int u) {
@@ -195,14 +190,14 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const CacheAtt
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int hk = blockIdx.y, b = blockIdx.z;
   const int64_t bh = (int64_t)b * p.H_kv + hk;
-  const int len = min(max(__ldg(p.len + b), 0), p.max_pages * kPage), nb = (len + kPage - 1) / kPage;
+  const int len = min(max(*(p.len + b), 0), p.max_pages * kPage), nb = (len + kPage - 1) / kPage;
   const int first = blockIdx.x * p.chunk, n = min(nb - first, p.chunk);
   const int64_t list = bh * p.n_chunk + blockIdx.x;
   if (n <= 0) {
     if (threadIdx.x == 0) p.chunk_n[list] = 0;
     return;
   }
-  const int row0 = __ldg(p.row + b), head = b * p.Hm + (p.Hm > 1 ? hk * p.group : 0);
+  const int row0 = *(p.row + b), head = b * p.Hm + (p.Hm > 1 ? hk * p.group : 0);
   for (int x0 = warp * kGang; x0 < n; x0 += kPlanThreads / 32 * kGang) {
     KeyBounds k[kGang][2];
     bool any[kGang], all[kGang];
@@ -210,7 +205,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const CacheAtt
 #pragma unroll
     for (int x = 0; x < kGang; ++x) {
       const int blk = first + min(x0 + x, n - 1);
-      page[x] = __ldg(p.page_table + (int64_t)b * p.max_pages + blk);
+      page[x] = *(p.page_table + (int64_t)b * p.max_pages + blk);
 #pragma unroll
       for (int i = 0; i < 2; ++i) load_pos(p, k[x][i], bh, blk * kPage + lane + 32 * i, len);
       any[x] = false;
@@ -355,7 +350,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
         unit_bh[u] = bh;
         if (u < 0 || u == nu) continue;
         const int b = bh / p.H_kv, hk = bh - b * p.H_kv;
-        const int len = min(max(__ldg(p.len + b), 0), cap);
+        const int len = min(max(*(p.len + b), 0), cap);
         int blk = at.y, partial = 0;
         if (p.masked) {
           const int w = __ldcg(p.listed + (int64_t)at.x * p.chunk + at.y);
@@ -364,13 +359,13 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
         } else {
           partial = (blk + 1) * kPage > len;
         }
-        int page = __ldg(p.page_table + (int64_t)b * p.max_pages + blk);
+        int page = *(p.page_table + (int64_t)b * p.max_pages + blk);
         const bool there = page >= 0 && page < p.n_pages;
         if (!there) page = 0;  // read, but no key of it is seen
         const int row = page * p.H_kv + hk;
         *reinterpret_cast<int2*>(&list[u]) = make_int2(row * kPage, blk * kPage + (there ? partial : 3));
-        scale_k[i] = there ? __ldg(p.k_scale + row) : 0.f;  // (stored once the ring has started)
-        scale_v[i] = there ? __ldg(p.v_scale + row) : 0.f;
+        scale_k[i] = there ? *(p.k_scale + row) : 0.f;  // (stored once the ring has started)
+        scale_v[i] = there ? *(p.v_scale + row) : 0.f;
         if (p.accumulate && !p.masked && chunk == 0) p.live[(int64_t)bh * p.max_pages + blk] = there;
       }
     }
@@ -427,7 +422,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
           const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + (((int64_t)b * p.n_q + tq) * p.H + h) * D) +
                                 lane * (kQElems / 2);
 #pragma unroll
-          for (int x = 0; x < kQElems / 2; ++x) qreg[i][x] = __ldg(src + x);
+          for (int x = 0; x < kQElems / 2; ++x) qreg[i][x] = *(src + x);
         }
       }
     };
@@ -511,7 +506,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
       if (sg >= 0) {
       const int bh = seg_bh[sg], flag = seg_flag[sg], e1 = seg_start[sg + 1];
       const int b = bh / p.H_kv, hk = bh % p.H_kv;
-      const int len = min(max(__ldg(p.len + b), 0), cap);
+      const int len = min(max(*(p.len + b), 0), cap);
       if (flag & kReset) {
         begun = flag;
 #pragma unroll
@@ -536,7 +531,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
           if (p.masked) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) load_pos(p, k[i], bh, slot0 + lane + 32 * i, len);
-            const int row0 = __ldg(p.row + b);
+            const int row0 = *(p.row + b);
             int at_head = -1;
             for (int n = 0; n < C::kRows; ++n) {
               const int r = min(row_base + n, p.n_rows - 1), hg = p.Hm > 1 ? r / p.n_q : 0;
@@ -897,7 +892,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const CacheAtt
   constexpr int kKeys = kWeightSlots / kJoinThreads;
   const int cap = p.max_pages * kPage, per_bh = (cap + kWeightSlots - 1) / kWeightSlots;
   const int w = blockIdx.x - n_join, bh = w / per_bh, s0 = w % per_bh * kWeightSlots, b = bh / p.H_kv;
-  const int len = min(max(__ldg(p.len + b), 0), cap);
+  const int len = min(max(*(p.len + b), 0), cap);
   const Span s = span_of(p, bh);
   float* weight = p.weight + (int64_t)bh * cap;
   float x[kKeys];
@@ -1017,13 +1012,8 @@ fm_status launch(const fm_kv_cache* c, CacheAttnParams p, cudaStream_t s) {
   CUtensorMap tk, tv;
   if (!encode_pool(&tk, c, c->k_codes) || !encode_pool(&tv, c, c->v_codes)) return FM_ERR_CUDA;
   if (!smem_opt_in<cache_attn_kernel<D, NT, E4M3>>(C::kAlloc)) return FM_ERR_CUDA;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  EarlyLaunch launch(s);
+  cudaLaunchConfig_t& cfg = launch.cfg;
   cudaError_t e;
   if (p.masked) {
     cfg.gridDim = dim3(p.n_chunk, p.H_kv, p.B);

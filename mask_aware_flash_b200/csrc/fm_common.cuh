@@ -418,6 +418,11 @@ __device__ __forceinline__ uint8_t* smem_base_1024(uint8_t* raw) {
   return raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
 }
 
+// Programmatic launches (EarlyLaunch below): a kernel may start while the one before it in the stream ends; it waits here for
+// that one's results before it reads anything, and lets the next one start.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // packed fp32 pairs (sm_100 f32x2 arithmetic); .x is the low half
 __device__ __forceinline__ uint64_t f2pack(float lo, float hi) {
   return ((uint64_t)__float_as_uint(hi) << 32) | __float_as_uint(lo);
@@ -590,5 +595,22 @@ bool encode_tmap_bf16_4d(CUtensorMap* map, const void* base, uint64_t D, uint64_
                          uint32_t box_rows);
 bool encode_tmap_f32_4d(CUtensorMap* map, const void* base, uint64_t D, uint64_t H, uint64_t n, uint64_t B,
                         uint32_t box_rows);
+// A launch whose kernel may start while the one before it in the stream ends (the kernel calls grid_wait), and of clusters of
+// `cluster` CTAs along x.
+struct EarlyLaunch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attrs[2];
+  explicit EarlyLaunch(cudaStream_t stream, int cluster = 1) {
+    cfg.stream = stream;
+    cfg.attrs = attrs;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = cluster;
+    attrs[1].val.clusterDim.y = 1;
+    attrs[1].val.clusterDim.z = 1;
+  }
+};
 bool encode_tmap_u8_rows(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_rows);
 }  // namespace fm

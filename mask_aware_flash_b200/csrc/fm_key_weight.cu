@@ -147,7 +147,7 @@ __device__ __forceinline__ void work_of(const KeyWeightParams& p, int w, int& bh
   bh = first + in % heads;
   const int b = bh / p.H_kv, hk = bh % p.H_kv;
   const int64_t bhm = (int64_t)b * p.Hm + (p.Hm == 1 ? 0 : hk * p.q_per_kv);
-  kt = __ldg(p.order + bhm * p.T_k + in / heads);
+  kt = *(p.order + bhm * p.T_k + in / heads);
 }
 
 template <int D>
@@ -191,6 +191,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   tc_fence_before();
+  grid_wait();
+  grid_launch_next();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = misc[0];
@@ -229,8 +231,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t* entries = p.col_entries + (bhm0 * p.T_k + kt) * p.T_q;
       // list lengths of the group's heads (at most 64) in two registers of the lanes, and their sum
       int n0 = 0, n1 = 0;
-      if (lane < p.q_per_kv) n0 = __ldg(counts + (p.Hm == 1 ? 0 : (int64_t)lane * p.T_k));
-      if (lane + 32 < p.q_per_kv) n1 = __ldg(counts + (p.Hm == 1 ? 0 : (int64_t)(lane + 32) * p.T_k));
+      if (lane < p.q_per_kv) n0 = *(counts + (p.Hm == 1 ? 0 : (int64_t)lane * p.T_k));
+      if (lane + 32 < p.q_per_kv) n1 = *(counts + (p.Hm == 1 ? 0 : (int64_t)(lane + 32) * p.T_k));
       const int total = __reduce_add_sync(0xffffffffu, n0 + n1);
       const int n_items = total > rank ? (total - rank + step - 1) / step : 0;  // of this CTA
 #pragma unroll
@@ -245,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int32_t* list = entries + (p.Hm == 1 ? 0 : (int64_t)hg * p.T_k * p.T_q);
         int at = skip;
         for (; at < n; at += 32 * step) {
-          const int mine = at + lane * step < n ? __ldg(list + at + lane * step) : 0;
+          const int mine = at + lane * step < n ? *(list + at + lane * step) : 0;
           const int here = min(32, (n - at + step - 1) / step);
           for (int j0 = 0; j0 < here; j0 += 8) {
             const int n_now = min(8, here - j0), entry = __shfl_sync(0xffffffffu, mine, j0 + (lane & 7));
@@ -396,8 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row = (e.x >> 1) * kTile + lane, h = (e.w & 0xFFFF) * p.q_per_kv + (e.y & 255);
       const float* src = p.lse + ((int64_t)((uint32_t)e.w >> 16) * p.H + h) * p.n_q + row;
       const int n = e.y & (kEmpty | kEnd) ? 0 : p.n_q - row;
-      return make_float4(n > 0 ? __ldg(src) : kNegInf, n > 32 ? __ldg(src + 32) : kNegInf, n > 64 ? __ldg(src + 64) : kNegInf,
-                         n > 96 ? __ldg(src + 96) : kNegInf);
+      return make_float4(n > 0 ? *src : kNegInf, n > 32 ? *(src + 32) : kNegInf, n > 64 ? *(src + 64) : kNegInf,
+                         n > 96 ? *(src + 96) : kNegInf);
     };
     // bounds of this thread's key for an item: lts, lte, uts, ute
     auto load_bounds = [&](const int4& e) {
@@ -406,10 +408,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t at = ((int64_t)b * p.Hm + hm) * p.n_k + key;
       const bool in = key < p.n_k && !(e.y & (kEmpty | kEnd));
       int4 v;
-      v.x = in && p.vec[0] ? __ldg(p.vec[0] + at) : p.n_q;
-      v.y = in && p.vec[1] ? __ldg(p.vec[1] + at) : p.n_q;
-      v.z = in && p.vec[2] ? __ldg(p.vec[2] + at) : 0;
-      v.w = in && p.vec[3] ? __ldg(p.vec[3] + at) : 0;
+      v.x = in && p.vec[0] ? *(p.vec[0] + at) : p.n_q;
+      v.y = in && p.vec[1] ? *(p.vec[1] + at) : p.n_q;
+      v.z = in && p.vec[2] ? *(p.vec[2] + at) : 0;
+      v.w = in && p.vec[3] ? *(p.vec[3] + at) : 0;
       return v;
     };
     int4 e_next, bounds_next;
@@ -530,18 +532,11 @@ fm_status launch_key_weight(const fm_attn_args* a, const KeyWeightParams& p, int
   // A key tile's query tiles are shared by a cluster of CTAs where there are too few key tiles for the SMs.
   int cluster = 1;
   while (cluster < 8 && (int64_t)p.n_work * cluster * 2 <= kSMs) cluster *= 2;
-  cudaLaunchConfig_t cfg = {};
+  EarlyLaunch launch(stream, cluster);
+  cudaLaunchConfig_t& cfg = launch.cfg;
   cfg.gridDim = dim3((unsigned)(cluster > 1 ? p.n_work * cluster : p.n_work < kSMs ? p.n_work : kSMs));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = S::kAlloc;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = cluster;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, key_weight_kernel<D>, tq, tk, p);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? FM_OK : FM_ERR_CUDA;
 }
