@@ -62,13 +62,16 @@ struct CacheAttnParams {
 
 template <int D, int NT>
 struct CacheAttnCfg {
-  static constexpr int kWarps = D == 256 ? 4 : 8;
+  // a warp's piece of work: a block, or half a one where a block's operands would leave the SM too few warps
+  static constexpr int kKeys = D == 256 && NT == 1 ? kPage / 2 : kPage;
+  static constexpr int kParts = kPage / kKeys;
+  static constexpr int kWarps = D == 256 && NT > 1 ? 4 : 8;
   static constexpr int kThreads = kWarps * 32;
   // ring slots of a warp (each one K or one V block): what shared memory holds
   static constexpr int kSlots = D == 64 ? 4 : 2;
   static constexpr int kBox = D < 128 ? D : 128;     // bytes of a TMA box row (= swizzle span)
   static constexpr int kBoxes = D / kBox;
-  static constexpr int kSlotBytes = kPage * D;
+  static constexpr int kSlotBytes = kKeys * D;
   static constexpr int kRows = 8 * NT;               // query rows a CTA holds
   static constexpr int kKSteps = D / 16;
   static constexpr int kCap = (256 + kThreads - 1) / kThreads * kThreads - 2;  // units listed at a time
@@ -144,10 +147,12 @@ __device__ __forceinline__ bool key_seen(const CacheAttnParams& p, const KeyBoun
   return k.in && !(p.causal && k.j > i) && !(k.lts <= i && i < k.lte) && !(k.uts <= i && i < k.ute);
 }
 
-// Units of a run: an equal share, but no fewer than the CTA has warps (a block per warp takes no longer than one block, and
-// there are fewer partial sums to join).
+// Units of a run: an equal share of all, but no fewer than fill the CTA's warps once (that takes no longer than one unit, and
+// leaves fewer partial sums to join) or than an equal cut of the average (sequence, head) into such pieces (short ones each
+// get a CTA of their own: a CTA takes those it holds one after the other).
 __device__ __forceinline__ int units_per_run(const CacheAttnParams& p, int total) {
-  return max((total + p.n_work - 1) / p.n_work, p.run_min);
+  const int average = total / (p.B * p.H_kv), pieces = max((average + p.run_min - 1) / p.run_min, 1);
+  return max(max((total + p.n_work - 1) / p.n_work, (average + pieces - 1) / pieces), 1);
 }
 
 // How many of the rows [i0, i1) see the key: those not before its pos (causal), less the union of its two stretches.
@@ -370,22 +375,20 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
       }
     }
     __syncthreads();
-    const int n_live = nu;
-
     // ---------------------------------------------------------------- the ring of this warp
-    const int n_items = 2 * (n_live > warp ? (n_live - warp + kWarps - 1) / kWarps : 0);
+    const int n_pieces = nu * C::kParts, n_items = 2 * (n_pieces > warp ? (n_pieces - warp + kWarps - 1) / kWarps : 0);
     int issued = 0, done = 0;
-    auto issue = [&]() {  // the next item: K of a block, then its V
+    auto issue = [&]() {  // the next item: K of a piece, then its V
       if (issued < n_items && ok) {
         if (lane == 0) {
-          const int4 e = list[warp + kWarps * (issued >> 1)];
+          const int piece = warp + kWarps * (issued >> 1), row = list[piece / C::kParts].x + piece % C::kParts * C::kKeys;
           const int slot = (item + issued) % kSlots;
           const uint32_t bar = bar0 + 8 * slot;
           mbar_arrive_expect_tx(bar, C::kSlotBytes);
 #pragma unroll
           for (int x = 0; x < C::kBoxes; ++x)
-            tma_load_2d(ring + slot * C::kSlotBytes + x * kPage * C::kBox, (issued & 1) ? &tm_v : &tm_k, bar, x * C::kBox,
-                        e.x);
+            tma_load_2d(ring + slot * C::kSlotBytes + x * C::kKeys * C::kBox, (issued & 1) ? &tm_v : &tm_k, bar, x * C::kBox,
+                        row);
         }
         ++issued;
       }
@@ -504,7 +507,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
       // the rows of the next segment: loaded here, in flight during this one, stored at the end of the loop's body
       if (sg + 1 < n_seg) load_q(seg_bh[sg + 1]);
       if (sg >= 0) {
-      const int bh = seg_bh[sg], flag = seg_flag[sg], e1 = seg_start[sg + 1];
+      const int bh = seg_bh[sg], flag = seg_flag[sg], e1 = seg_start[sg + 1] * C::kParts;
       const int b = bh / p.H_kv, hk = bh % p.H_kv;
       const int len = min(max(*(p.len + b), 0), cap);
       if (flag & kReset) {
@@ -521,8 +524,8 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
         unit_v = max_v = 0.f;
       }
       for (int e = warp + kWarps * (done >> 1); e < e1; e += kWarps) {
-        const int4 ent = list[e];
-        const int slot0 = ent.y & ~3;
+        const int4 ent = list[e / C::kParts];
+        const int slot0 = (ent.y & ~3) + e % C::kParts * C::kKeys;
         const bool partial = ent.y & 1, missing = ent.y & 2;
         const float ks = __int_as_float(ent.z), vs = __int_as_float(ent.w);
         if (partial) {
@@ -530,20 +533,29 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
           KeyBounds k[2];
           if (p.masked) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) load_pos(p, k[i], bh, slot0 + lane + 32 * i, len);
+            for (int i = 0; i < C::kKeys / 32; ++i) load_pos(p, k[i], bh, slot0 + lane + 32 * i, len);
             const int row0 = *(p.row + b);
-            int at_head = -1;
+            // row row_base + n is query tq of head hg of the group (rows behind the last one take its bits)
+            int hg = row_base / p.n_q, tq = row_base - hg * p.n_q;
+            bool new_head = true;
+            uint32_t lo = 0, hi = 0;
+#pragma unroll 1
             for (int n = 0; n < C::kRows; ++n) {
-              const int r = min(row_base + n, p.n_rows - 1), hg = p.Hm > 1 ? r / p.n_q : 0;
-              if (hg != at_head) {
-                at_head = hg;
-                const int64_t bhm = p.Hm > 1 ? (int64_t)b * p.Hm + hk * p.group + hg : b;
+              if (row_base + n < p.n_rows) {
+                if (new_head) {
+                  const int64_t bhm = p.Hm > 1 ? (int64_t)b * p.Hm + hk * p.group + hg : b;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) load_vectors(p, k[i], bhm);
+                  for (int i = 0; i < C::kKeys / 32; ++i) load_vectors(p, k[i], bhm);
+                }
+                lo = __ballot_sync(0xffffffffu, key_seen(p, k[0], row0 + tq));
+                hi = C::kKeys == 64 ? __ballot_sync(0xffffffffu, key_seen(p, k[1], row0 + tq)) : 0u;
+                new_head = false;
+                if (++tq == p.n_q) {
+                  tq = 0;
+                  ++hg;
+                  new_head = p.Hm > 1;
+                }
               }
-              const int i = row0 + r % p.n_q;
-              const uint32_t lo = __ballot_sync(0xffffffffu, key_seen(p, k[0], i));
-              const uint32_t hi = __ballot_sync(0xffffffffu, key_seen(p, k[1], i));
               if (lane == (n & 31)) bits_s[n] = make_uint2(lo, hi);
             }
           } else {
@@ -553,11 +565,12 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
           }
           __syncwarp();
         }
-        // ------------------------------------------------------------ S^T = K Q^T (64 keys x rows)
+        // ------------------------------------------------------------ S^T = K Q^T (the piece's keys x rows)
         wait();
-        float s[4][NT][4];
+        constexpr int kJ = C::kKeys / 16;  // 16-key tiles of the piece
+        float s[kJ][NT][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < kJ; ++j)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -571,14 +584,14 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
             for (int h = 0; h < (C::kBox == 128 ? 2 : 1); ++h) {
               // key 16 j + 8 r + g, 16-byte piece 2 t + h (t for D = 64): no two lanes of a quarter warp
               // share a bank under the swizzle
-              uint4 raw[4][2];
+              uint4 raw[kJ][2];
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
+              for (int j = 0; j < kJ; ++j)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                   const int key = 16 * j + 8 * r + g;
                   const int c = C::kBox == 128 ? ((2 * t + h) ^ (key & 7)) : (t ^ ((key >> 1) & 3));
-                  raw[j][r] = *reinterpret_cast<const uint4*>(kb + x * kPage * C::kBox + key * C::kBox + c * 16);
+                  raw[j][r] = *reinterpret_cast<const uint4*>(kb + x * C::kKeys * C::kBox + key * C::kBox + c * 16);
                 }
 #pragma unroll
               for (int w = 0; w < 4; ++w) {
@@ -587,7 +600,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) bq[nt] = q_s[(nt * C::kKSteps + step) * 32 + lane];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < kJ; ++j) {
                   const uint32_t wa = w == 0 ? raw[j][0].x : w == 1 ? raw[j][0].y : w == 2 ? raw[j][0].z : raw[j][0].w;
                   const uint32_t wb = w == 0 ? raw[j][1].x : w == 1 ? raw[j][1].y : w == 2 ? raw[j][1].z : raw[j][1].w;
                   uint32_t a0, a1, a2, a3;
@@ -603,7 +616,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
         issue();  // K's slot is free
         ++done;
         // ------------------------------------------------------------ softmax: this thread's rows 2t, 2t+1
-        uint32_t pb[4][NT][2];  // P^T fragments
+        uint32_t pb[kJ][NT][2];  // P^T fragments
         bool moved = false;
         float alpha[NT][2];
         const float unit_new = vs > 0.f ? fmaxf(vs, fmaxf(max_v, vs) * 9.094947e-13f) : unit_v;  // 2^-40: see below
@@ -614,14 +627,14 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
           for (int x = 0; x < 2; ++x) {
             const float cf = qs_s[nt * 8 + 2 * t + x] * ks;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < kJ; ++j) {
               s[j][nt][x] *= cf;
               s[j][nt][2 + x] *= cf;
             }
             if (partial) {
               const uint2 bits = bits_s[nt * 8 + 2 * t + x];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
+              for (int j = 0; j < kJ; ++j) {
                 const uint32_t w = j < 2 ? bits.x : bits.y;
                 if (!((w >> (16 * (j & 1) + g)) & 1u)) s[j][nt][x] = kNegInf;
                 if (!((w >> (16 * (j & 1) + 8 + g)) & 1u)) s[j][nt][2 + x] = kNegInf;
@@ -631,7 +644,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
           if (p.accumulate && row_base + nt * 8 + 2 * t < p.rows4) {
             float* dst = p.score + ((int64_t)bh * cap + slot0 + g) * p.rows4 + row_base + nt * 8 + 2 * t;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < kJ; ++j) {
               *reinterpret_cast<float2*>(dst + (int64_t)(16 * j) * p.rows4) = make_float2(s[j][nt][0], s[j][nt][1]);
               *reinterpret_cast<float2*>(dst + (int64_t)(16 * j + 8) * p.rows4) = make_float2(s[j][nt][2], s[j][nt][3]);
             }
@@ -640,7 +653,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
           for (int x = 0; x < 2; ++x) {
             float mx = fmaxf(s[0][nt][x], s[0][nt][2 + x]);
 #pragma unroll
-            for (int j = 1; j < 4; ++j) mx = fmaxf(mx, fmaxf(s[j][nt][x], s[j][nt][2 + x]));
+            for (int j = 1; j < kJ; ++j) mx = fmaxf(mx, fmaxf(s[j][nt][x], s[j][nt][2 + x]));
 #pragma unroll
             for (int y = 4; y < 32; y <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
             const float m_new = fmaxf(m[nt][x], mx - kPBias);
@@ -650,7 +663,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
             m[nt][x] = m_new;
             float sum = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < kJ; ++j) {
               s[j][nt][x] = ex2(s[j][nt][x] - m_use);
               s[j][nt][2 + x] = ex2(s[j][nt][2 + x] - m_use);
               sum += s[j][nt][x] + s[j][nt][2 + x];
@@ -658,7 +671,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
             l[nt][x] = fmaf(l[nt][x], alpha[nt][x], sum);
           }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {  // keys 16 j + 2t, +1 and + 8, + 9 of row g, as the product reads them
+          for (int j = 0; j < kJ; ++j) {  // keys 16 j + 2t, +1 and + 8, + 9 of row g, as the product reads them
             pb[j][nt][0] = transpose8x8(pack_f16(s[j][nt][0] * p_scale, s[j][nt][1] * p_scale));
             pb[j][nt][1] = transpose8x8(pack_f16(s[j][nt][2] * p_scale, s[j][nt][3] * p_scale));
           }
@@ -687,10 +700,10 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
         {
           uint8_t* vb = ring_p + (item + done) % kSlots * C::kSlotBytes;
           const int valid = missing ? 0 : len - slot0;
-          if (partial && valid < kPage) {  // slots never written may hold any bytes, a NaN's among them
-            for (int x = lane; x < (kPage - valid) * (D / 16); x += 32) {
-              const int row = valid + x / (D / 16), piece = x % (D / 16);
-              *reinterpret_cast<uint4*>(vb + piece / (C::kBox / 16) * kPage * C::kBox + row * C::kBox + piece % (C::kBox / 16) * 16) =
+          if (partial && valid < C::kKeys) {  // slots never written may hold any bytes, a NaN's among them
+            for (int x = lane; x < (C::kKeys - max(valid, 0)) * (D / 16); x += 32) {
+              const int row = max(valid, 0) + x / (D / 16), piece = x % (D / 16);
+              *reinterpret_cast<uint4*>(vb + piece / (C::kBox / 16) * C::kKeys * C::kBox + row * C::kBox + piece % (C::kBox / 16) * 16) =
                   make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();  // (the slot's next copy comes after these)
@@ -700,13 +713,13 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
 #pragma unroll
           for (int x = 0; x < C::kBoxes; ++x)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < kJ; ++j) {
               uint32_t raw[4][kWords];  // keys 16 j + 2t, + 1, + 8, + 9
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
                 const int key = 16 * j + 2 * t + (r & 1) + 8 * (r >> 1);
                 if constexpr (C::kBox == 128) {
-                  const uint4 v = *reinterpret_cast<const uint4*>(vb + x * kPage * 128 + key * 128 + ((g ^ (key & 7)) << 4));
+                  const uint4 v = *reinterpret_cast<const uint4*>(vb + x * C::kKeys * 128 + key * 128 + ((g ^ (key & 7)) << 4));
                   raw[r][0] = v.x;
                   raw[r][1] = v.y;
                   raw[r][2] = v.z;
@@ -999,18 +1012,18 @@ fm_status check_cache_attn(const fm_kv_cache* c, const fm_cache_attn_args* a) {
   return FM_OK;
 }
 
-// Tensor map over a code pool: rows of D bytes (page, head, slot), boxes of 64 rows, 64- or 128-byte swizzle.
-bool encode_pool(CUtensorMap* map, const fm_kv_cache* c, const void* base) {
-  return encode_tmap_u8_rows(map, base, c->D, (uint64_t)c->n_pages * c->H_kv * kPage, kPage);
+// Tensor map over a code pool: rows of D bytes (page, head, slot), boxes of a piece's keys, 64- or 128-byte swizzle.
+bool encode_pool(CUtensorMap* map, const fm_kv_cache* c, const void* base, int keys) {
+  return encode_tmap_u8_rows(map, base, c->D, (uint64_t)c->n_pages * c->H_kv * kPage, keys);
 }
 
 template <int D, int NT, bool E4M3>
 fm_status launch(const fm_kv_cache* c, CacheAttnParams p, cudaStream_t s) {
   using C = CacheAttnCfg<D, NT>;
-  p.run_min = C::kWarps;
+  p.run_min = C::kWarps / C::kParts;
   static_assert(C::kAlloc <= 227 * 1024, "shared memory exceeds the per-CTA limit");
   CUtensorMap tk, tv;
-  if (!encode_pool(&tk, c, c->k_codes) || !encode_pool(&tv, c, c->v_codes)) return FM_ERR_CUDA;
+  if (!encode_pool(&tk, c, c->k_codes, C::kKeys) || !encode_pool(&tv, c, c->v_codes, C::kKeys)) return FM_ERR_CUDA;
   if (!smem_opt_in<cache_attn_kernel<D, NT, E4M3>>(C::kAlloc)) return FM_ERR_CUDA;
   EarlyLaunch launch(s);
   cudaLaunchConfig_t& cfg = launch.cfg;
