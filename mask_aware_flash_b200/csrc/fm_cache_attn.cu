@@ -94,6 +94,7 @@ struct CacheAttnCfg {
   static constexpr int kBefore = kRed + 128;                            // int [threads]: units before each thread's lists
   static constexpr int kBytes = kBefore + kThreads * 4;
   static constexpr int kAlloc = kBytes + 1024;
+  static_assert(kList % 16 == 0 && kMl % 8 == 0 && kBits % 8 == 0 && kBar % 8 == 0, "shared memory alignment");
 };
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
@@ -814,7 +815,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
 // Last kernel (it may be resident before the one before ends, so what that wrote is read through L2).  The first CTAs join
 // the rows of the (sequence, head)s that several runs share, a CTA per row; the others add the softmax weights of kWeightSlots keys each to the cache's, from the stored scores.
 constexpr int kJoinThreads = 128;
-constexpr int kWeightSlots = 512;
+constexpr int kWeightSlots = 1024;
 constexpr int kMaxRows = 1024;
 
 struct Span {  // the runs that hold a (sequence, head), and where their partial sums are

@@ -57,7 +57,7 @@ def _call(fn, what, device, stream, *args):
 
 def _expect(what, device, name, t, dtype, shape):
     """One tensor of a call: on `device`, contiguous, of that type and shape (_check_tensors words the error)."""
-    if not (t.is_cuda and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+    if not (t.dtype is dtype and t.device == device and t.shape == shape and t.is_contiguous()):
         _check_tensors(what, device, [(name, t, dtype, shape)])
 
 
