@@ -27,7 +27,7 @@ constexpr int kListWarp = kGroups * 4, kLoadWarp = kListWarp + 1, kMmaWarp = kLi
 constexpr int kSMs = 148;
 constexpr int kBufs = kGroups;  // TMEM score buffers of 128 columns, one per warpgroup
 constexpr int kRing = 8;      // listed items of a reader
-constexpr int kReaders = kGroups + 2;  // the warpgroups of sums, the load and the MMA role
+constexpr int kReaders = kGroups + 1;  // the warpgroups of sums, the load role
 constexpr float kNegInf = -__builtin_huge_valf();
 
 struct KeyWeightParams {
@@ -59,14 +59,26 @@ struct KeyWeightSmem {
          S_FULL = Q_EMPTY + kStages, S_EMPTY = S_FULL + kBufs, ITEM = S_EMPTY + kBufs, ITEM_FREE = ITEM + kReaders * kRing,
          SUM_FULL = ITEM_FREE + kReaders * kRing, SUM_EMPTY = SUM_FULL + 2, DRAIN = SUM_EMPTY + 2, kNumBars };
   static constexpr int kMisc = kBar + kNumBars * 8;  // [0] TMEM base, [1] abort flag, [2] zero
-  static constexpr int kBytes = kMisc + 16;
+  static constexpr int kFlags = kMisc + 16;          // int [kStages]: flags of the query tiles in flight
+  static constexpr int kBytes = kFlags + kStages * 4;
   static constexpr int kAlloc = kBytes + 1024;
 };
 // An item: .x query-tile entry (qt << 1 | partial), .y query head of the group and flags, .z key tile, .w b << 16 | hk.
-// Each reader has a ring of its own: the load and MMA roles get every query tile, with kFirst and kLast of its key tile; a
+// Each reader has a ring of its own: the load role gets every query tile, with kFirst and kLast of its key tile (and passes
+// those on to the MMA role with the tile); a
 // warpgroup of sums gets its query tiles, with kLast at its last one of the key tile, or a kLast | kEmpty item if it has none.
 constexpr int kFirst = 1 << 8, kLast = 2 << 8, kEmpty = 4 << 8, kEnd = 8 << 8;
 
+// One lane of a converged warp (the same one every time).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xFFFFFFFF;\n\t"
+      "selp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
 // Has the phase of the given parity completed?  (Never waits, as try_wait may.)
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -171,6 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* lse_s = reinterpret_cast<float*>(smem + S::kLse);
   float* sum_s = reinterpret_cast<float*>(smem + S::kSum);
   int4* items = reinterpret_cast<int4*>(smem + S::kItems);
+  volatile int* stage_flags = reinterpret_cast<volatile int*>(smem + S::kFlags);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kNumBars; ++i) mbar_init(bar(i), 1);
@@ -255,7 +268,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int q = qi + lane, reader = q % kGroups, i = item + lane;
               const int4 e = make_int4(entry, hg | (i == 0 ? kFirst : 0) | (i + 1 == n_items ? kLast : 0), kt, b_hk);
               put(kGroups, q, e);
-              put(kGroups + 1, q, e);
               int n_before = pushed[0];
 #pragma unroll
               for (int g = 1; g < kGroups; ++g) n_before = reader == g ? pushed[g] : n_before;
@@ -286,7 +298,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < kGroups; ++i) put(i, pushed[i], make_int4(0, kEnd, 0, 0));
       put(kGroups, qi, make_int4(0, kEnd, 0, 0));
-      put(kGroups + 1, qi, make_int4(0, kEnd, 0, 0));
     }
     if (!ok && lane == 0) record_failure(p.status, abort_flag, 61);
   } else if (warp == kLoadWarp) {
@@ -302,7 +313,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int4 e = items[slot];
         mbar_arrive(bar(S::ITEM_FREE + slot));
-        if (e.y & kEnd) break;
         const int b = (int)((uint32_t)e.w >> 16), hk = e.w & 0xFFFF;
         const int kb = wk % S::kKBufs, st = qi % S::kStages;
         if ((e.y & kFirst) && wk >= S::kKBufs && !mbar_wait_idle(bar(S::K_EMPTY + kb), (wk / S::kKBufs - 1) & 1, abort_flag)) {
@@ -319,6 +329,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
+        stage_flags[st] = e.y;
+        if (e.y & kEnd) {  // (the MMA role's end: a stage without a tile)
+          mbar_arrive(bar(S::Q_FULL + st));
+          break;
+        }
         mbar_arrive_expect_tx(bar(S::Q_FULL + st), S::kTileBytes);
         for (int c = 0; c < kAtoms; ++c)
           tma_load_4d(q_s + st * S::kTileBytes + c * 16384, &tm_q, bar(S::Q_FULL + st), c * 64,
@@ -328,51 +343,49 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) record_failure(p.status, abort_flag, 64);
       // the copies in flight land before this role ends (a consumer that gave up may leave some unread)
       for (int x = max(wk - S::kKBufs, 0); x < wk; ++x) mbar_wait(bar(S::K_FULL + x % S::kKBufs), (x / S::kKBufs) & 1, never);
-      for (int x = max(qi - S::kStages, 0); x < qi; ++x) mbar_wait(bar(S::Q_FULL + x % S::kStages), (x / S::kStages) & 1, never);
+      // (the end's stage held the tile kStages before, which the wait for the stage has seen through)
+      for (int x = max(qi - S::kStages + (ok ? 1 : 0), 0); x < qi; ++x)
+        mbar_wait(bar(S::Q_FULL + x % S::kStages), (x / S::kStages) & 1, never);
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------- MMA role
-    if (lane == 0) {
-      constexpr uint32_t kIdesc = idesc_bf16(128, 128, false, false);
-      constexpr uint32_t kHi = desc_hi(1024);
-      const uint32_t lo_k = desc_lo(k_s, 16), lo_q = desc_lo(q_s, 16);
-      bool ok = true;
-      int qi = 0, wk = 0;
-      for (int it = 0;; ++it) {
-        const int slot = (kGroups + 1) * kRing + it % kRing;
-        if (!mbar_wait_idle(bar(S::ITEM + slot), (it / kRing) & 1, abort_flag)) {
-          ok = false;
-          break;
-        }
-        const int flags = items[slot].y;
-        mbar_arrive(bar(S::ITEM_FREE + slot));
-        if (flags & kEnd) break;
-        const int st = qi % S::kStages, buf = qi % kBufs, kb = wk % S::kKBufs;
-        if (((flags & kFirst) && !mbar_wait_idle(bar(S::K_FULL + kb), (wk / S::kKBufs) & 1, abort_flag)) ||
-            !mbar_wait_idle(bar(S::Q_FULL + st), (qi / S::kStages) & 1, abort_flag) ||
-            (qi >= kBufs && !mbar_wait_idle(bar(S::S_EMPTY + buf), (qi / kBufs - 1) & 1, abort_flag))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t qa = lo_q + st * (S::kTileBytes >> 4), ka = lo_k + kb * (S::kTileBytes >> 4);
+    // The whole warp runs it, so that descriptors and addresses stay in uniform registers; one elected lane issues.
+    constexpr uint32_t kIdesc = idesc_bf16(128, 128, false, false);
+    constexpr uint32_t kHi = desc_hi(1024);
+    const uint32_t lo_k = desc_lo(k_s, 16), lo_q = desc_lo(q_s, 16);
+    bool ok = true;
+    int wk = 0;
+    for (int qi = 0;; ++qi) {
+      const int st = qi % S::kStages, buf = qi % kBufs, kb = wk % S::kKBufs;
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(S::Q_FULL + st), (qi / S::kStages) & 1, abort_flag));
+      if (!ok) break;
+      const int flags = __shfl_sync(0xffffffffu, stage_flags[st], 0);
+      if (flags & kEnd) break;
+      ok = (!(flags & kFirst) || mbar_wait(bar(S::K_FULL + kb), (wk / S::kKBufs) & 1, abort_flag)) &&
+           (qi < kBufs || mbar_wait(bar(S::S_EMPTY + buf), (qi / kBufs - 1) & 1, abort_flag));
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t qa = lo_q + st * (S::kTileBytes >> 4), ka = lo_k + kb * (S::kTileBytes >> 4);
+      if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
           umma_ss_w(tmem + buf * 128, ka + off, kHi, qa + off, kHi, kIdesc, k > 0 ? 1u : 0u);
         }
-        umma_commit(bar(S::Q_EMPTY + st));
         umma_commit(bar(S::S_FULL + buf));
-        ++qi;
-        if (flags & kLast) {
-          umma_commit(bar(S::K_EMPTY + kb));
-          ++wk;
-        }
+        umma_commit(bar(S::Q_EMPTY + st));
+        if (flags & kLast) umma_commit(bar(S::K_EMPTY + kb));
       }
-      if (!ok) record_failure(p.status, abort_flag, 62);
+      __syncwarp();
+      if (flags & kLast) ++wk;
+    }
+    if (!ok && lane == 0) record_failure(p.status, abort_flag, 62);
+    if (elect_one()) {
       umma_commit(bar(S::DRAIN));  // every MMA has finished before TMEM is released
       mbar_wait(bar(S::DRAIN), 0, never);
     }
+    __syncwarp();
   } else {
     // ------------------------------------------------------- exponentials and sums: one key per thread
     const int wg = warp >> 2, r = threadIdx.x & 127;
