@@ -314,7 +314,7 @@ fm_status fm_attn_bwd_noalloc(const fm_attn_args* a, const fm_mask_meta* meta, c
  *   scale is 0 if amax = 0, else the smallest power of two 2^e >= amax / Qmax, e >= -126; codes are
  *   x / scale rounded to nearest, ties to even, after clamping to [-Qmax, Qmax] (so infinities
  *   saturate); NaN becomes 0.  Powers of two make the division exact, so a code has one rounding.
- *   D is 64, 128 or 256; n_pages * H_kv * 64 and B * H_kv * max_pages * 64 are below 2^31; B, H_kv <= 65535.
+ *   D is 64, 128 or 256; n_pages * H_kv * 64 is below 2^31, B * H_kv * max_pages * 64 below 2^30; B, H_kv <= 65535.
  */
 typedef struct {
   int32_t B, H_kv, D, n_pages, max_pages;
@@ -407,7 +407,7 @@ size_t fm_cache_evict_workspace_bytes(const fm_kv_cache* src, int32_t budget);
  * keeps all its slots.  What is kept goes, in slot order, to slots 0, 1, ... of dst with its weight and
  * pos, each dst block re-quantised by the scale rule over the values it now holds; slots behind the
  * last one in its block get code 0, whole blocks behind it and their weight and pos are not written.
- * new_len[b] = min(len[b], budget).
+ * new_len[b] = min(len[b], budget).  (A kept slot whose dst page is not there leaves its weight and pos only.)
  *   src, dst  same B, H_kv, D, code_type; src->weight is needed; dst may lie in the same pools
  *             as src, with a table of other pages: a page of dst must not be a page of src that is in
  *             use.  dst->weight and dst->pos may be NULL; src->pos NULL = the slot index.

@@ -10,9 +10,10 @@ fm_status check_cache(const fm_kv_cache* c) {
   if (c->code_type != 0 && c->code_type != 1) return FM_ERR_UNSUPPORTED;
   if (c->D != 64 && c->D != 128 && c->D != 256) return FM_ERR_UNSUPPORTED;
   if (c->B > kMaxCacheB || c->H_kv > 65535) return FM_ERR_UNSUPPORTED;
-  constexpr int64_t kLimit = (int64_t)1 << 31;
-  if ((int64_t)c->n_pages * c->H_kv >= kLimit / kPage) return FM_ERR_UNSUPPORTED;
-  if ((int64_t)c->B * c->H_kv >= kLimit / kPage || (int64_t)c->B * c->H_kv * c->max_pages >= kLimit / kPage)
+  // rows of the pools, and slots of the tables, in 32 bits; the slots with room for the strides that loops add to them
+  if ((int64_t)c->n_pages * c->H_kv >= ((int64_t)1 << 31) / kPage) return FM_ERR_UNSUPPORTED;
+  constexpr int64_t kSlotPages = ((int64_t)1 << 30) / kPage;
+  if ((int64_t)c->B * c->H_kv >= kSlotPages || (int64_t)c->B * c->H_kv * c->max_pages >= kSlotPages)
     return FM_ERR_UNSUPPORTED;
   if (!c->k_codes || !c->v_codes || !c->k_scale || !c->v_scale || !c->page_table) return FM_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(c->k_codes) | reinterpret_cast<uintptr_t>(c->v_codes)) & 15) return FM_ERR_INVALID_ARG;

@@ -15,10 +15,12 @@ has grown over its budget.
     fm_cache_append(smaller, k1, v1, start=new_len, row=position)   # one token
     o1, lse1 = fm_cache_attn(smaller, q1, new_len + 1, scale, row=position, vecs=vecs, accumulate=True)
 
-As everywhere in the package the caller owns the buffers; work runs on the current stream of the cache's device.
+As everywhere in the package the caller owns the buffers; work runs on the current stream of the cache's device, or on the
+one given.  What a call allocates itself belongs to that stream.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import sys
 
@@ -53,6 +55,12 @@ def _call(fn, what, device, stream, *args):
             code = fn(*args, raw)
     if code:
         _check(code, what)
+
+
+def _allocating(stream):
+    """What a call allocates belongs to the stream it runs on: memory that this stream's allocator hands out has no work of
+    another stream pending, and what is dropped (a workspace) is handed out again in this stream's order only."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _expect(what, device, name, t, dtype, shape):
@@ -183,19 +191,21 @@ def fm_cache_attn(cache: KVCache, q, cache_len, scale, row=None, vecs=None, caus
     _expect(what, dev, "cache_len", cache_len, torch.int32, batch)
     if row is not None:
         _expect(what, dev, "row", row, torch.int32, batch)
-    if o is None:
-        o = torch.empty_like(q)
-    else:
+    if o is not None:
         _expect(what, dev, "o", o, torch.bfloat16, shape)
-    if lse is None:
-        lse = torch.empty(rows, dtype=torch.float32, device=dev)
-    else:
+    if lse is not None:
         _expect(what, dev, "lse", lse, torch.float32, rows)
     if ws is not None:
         _expect(what, dev, "ws", ws, torch.uint8, ws.shape)
     L, ref = _lib(), ctypes.byref(a)
-    if ws is None:
-        ws = torch.empty(max(int(L.fm_cache_attn_workspace_bytes(cache._ref, ref)), 1), dtype=torch.uint8, device=q.device)
+    if o is None or lse is None or ws is None:
+        with _allocating(stream):
+            if o is None:
+                o = torch.empty_like(q)
+            if lse is None:
+                lse = torch.empty(rows, dtype=torch.float32, device=dev)
+            if ws is None:
+                ws = torch.empty(max(int(L.fm_cache_attn_workspace_bytes(cache._ref, ref)), 1), dtype=torch.uint8, device=dev)
     _call(L.fm_cache_attn, what, cache.device, stream, cache._ref, ref, o.data_ptr(), lse.data_ptr(), ws.data_ptr(),
           ws.numel())
     return o, lse
@@ -214,7 +224,8 @@ def fm_attn_key_weight(q, k, lse, meta: MaskMeta, vecs, scale, weight=None, accu
     if weight is None:
         if accumulate:
             raise FmError(FM_ERR_INVALID_ARG, f"{what}: accumulate needs a weight to add to")
-        weight = torch.empty((B, H_kv, n_k), dtype=torch.float32, device=q.device)
+        with _allocating(stream):
+            weight = torch.empty((B, H_kv, n_k), dtype=torch.float32, device=q.device)
     if weight.dim() != 3 or weight.shape[2] < n_k:
         raise FmError(FM_ERR_INVALID_ARG, f"{what}: weight must be [B, H_kv, >= n_k]")
     d, dev = meta.desc, q.device
@@ -245,19 +256,21 @@ def fm_cache_evict(src: KVCache, dst: KVCache, cache_len, budget: int, recent: i
         raise FmError(FM_ERR_INVALID_ARG, f"{what}: src has no weight to go by")
     if (src.B, src.H_kv, src.D, src.k_codes.dtype) != (dst.B, dst.H_kv, dst.D, dst.k_codes.dtype):
         raise FmError(FM_ERR_INVALID_ARG, f"{what}: src and dst must agree in B, H_kv, D and code type")
-    if new_len is None:
-        new_len = torch.empty_like(cache_len)
     dev = src.device
     _expect(what, dev, "cache_len", cache_len, torch.int32, src.batch)
-    _expect(what, dev, "new_len", new_len, torch.int32, src.batch)
+    if new_len is not None:
+        _expect(what, dev, "new_len", new_len, torch.int32, src.batch)
     if ws is not None:
         _expect(what, dev, "ws", ws, torch.uint8, ws.shape)
     if dst.device != dev:
         raise FmError(FM_ERR_INVALID_ARG, f"{what}: src and dst must be on one device")
     L = _lib()
-    if ws is None:
-        n = int(L.fm_cache_evict_workspace_bytes(src._ref, int(budget)))
-        ws = torch.empty(max(n, 1), dtype=torch.uint8, device=src.device)
+    with _allocating(stream):
+        if new_len is None:
+            new_len = torch.empty_like(cache_len)
+        if ws is None:
+            n = int(L.fm_cache_evict_workspace_bytes(src._ref, int(budget)))
+            ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
     _call(L.fm_cache_evict, what, src.device, stream, src._ref, dst._ref, cache_len.data_ptr(), int(budget), int(recent),
           new_len.data_ptr(), ws.data_ptr(), ws.numel())
     return new_len

@@ -431,6 +431,171 @@ def test_attention_pool_beyond_32_bits(fm):
         assert ((lse[0, 2 * hk:2 * hk + 2, 0].double() - L).abs() <= delta + 40000 * 2.0 ** -24 + 2.0 ** -22 * L.abs()).all()
 
 
+def shared_page_cache(fm, B, H_kv, D, max_pages, n_pages, code, g, weight=False):
+    """A cache whose table entries point at few pages, many sequences at the same ones (as prompts that share a prefix do)."""
+    pools = [torch.randint(-100, 101, (n_pages, H_kv, PAGE, D), generator=g, device="cuda", dtype=torch.int8) for _ in range(2)]
+    if code == "e4m3":
+        pools = [(p.float() / 16).to(torch.float8_e4m3fn) for p in pools]
+    scales = [torch.exp2(torch.randint(-8, -4, (n_pages, H_kv), generator=g, device="cuda").float()) for _ in range(2)]
+    table = torch.randint(0, n_pages, (B, max_pages), generator=g, device="cuda", dtype=torch.int32)
+    w = torch.rand((B, H_kv, max_pages * PAGE), generator=g, device="cuda") if weight else None
+    return fm.KVCache(*pools, *scales, table, weight=w)
+
+
+def check_sequence(cache, b, hk, n, q, o, lse, scale, ok=None):
+    """One (sequence, K/V head) against float64 torch, with the bounds above.  q [n_q, G, D], o likewise, lse [G, n_q];
+    ok [n_q, n]: which keys each query sees."""
+    pages = cache.page_table[b, :-(-n // PAGE)].long()
+    K, V = ((c[pages, hk].double() * s[pages, hk].double()[:, None, None]).reshape(-1, cache.D)[:n]
+            for c, s in ((cache.k_codes, cache.k_scale), (cache.v_codes, cache.v_scale)))
+    qd = q.double()
+    s = scale * torch.einsum("tgd,nd->tgn", qd, K)
+    mag = scale * torch.einsum("tgd,nd->tgn", qd.abs(), K.abs())
+    if ok is not None:
+        s = s.masked_fill(~ok[:, None, :], float("-inf"))
+        mag = mag.masked_fill(~ok[:, None, :], 0)
+    L = torch.logsumexp(s, -1)
+    live = torch.isfinite(L)
+    p = torch.where(live[..., None], torch.exp(s - torch.where(live, L, 0)[..., None]), 0)
+    delta = (cache.D + 8) * 2.0 ** -23 * mag.amax(-1) + 2.0 ** -20
+    O, absum = torch.einsum("tgn,nd->tgd", p, V), torch.einsum("tgn,nd->tgd", p, V.abs())
+    tol = 2.0 ** -8 * O.abs() + (2.0 ** -11 + 2 * delta + n * 2.0 ** -23)[..., None] * absum + 1e-37
+    assert ((o.double() - O).abs() <= tol).all(), f"sequence {b} head {hk}: O off by {(o.double() - O).abs().max()}"
+    got = lse.double().T
+    assert torch.isneginf(got[~live]).all()
+    assert ((got - L)[live].abs() <= (delta + n * 2.0 ** -24 + 2.0 ** -22 * L.abs())[live]).all()
+
+
+def test_attention_many_sequences_and_long_masks(fm):
+    """More (sequence, head) lists than threads, chunks of more than 64 blocks, masks over several chunks, empty sequences."""
+    B, H_kv, G, D, max_pages, n_q = 520, 8, 2, 64, 200, 2
+    g = torch.Generator(device="cuda").manual_seed(3)
+    cache = shared_page_cache(fm, B, H_kv, D, max_pages, 60, "int8", g)
+    r = np.random.default_rng(3)
+    lens = r.integers(0, 300, B)
+    lens[[5, 77, 519]] = [12000, 12800, 9001]
+    n = int(max_pages * PAGE)
+    j = np.arange(n)
+    vecs = [np.broadcast_to(x, (B, 1, n)).astype(np.int32) for x in (np.minimum(j + 3000, n), np.full(n, n), np.zeros(n), j)]
+    vecs[0][:, :, :200] = n  # the first keys stay visible: the seen blocks are two stretches of the list
+    vt = [torch.from_numpy(np.ascontiguousarray(x)).cuda() for x in vecs]
+    q = torch.randn((B, n_q, H_kv * G, D), generator=g, device="cuda").to(torch.bfloat16)
+    row = np.maximum(lens - n_q, 0)
+    o, lse = fm.fm_cache_attn(cache, q, i32(lens), 0.125, row=i32(row), vecs=vt)
+    assert fm.fm_get_device_status() == 0
+    for b in (0, 5, 77, 300, 518, 519):
+        m = int(lens[b])
+        if m == 0:
+            continue
+        ok = torch.from_numpy(ref.seen(np.arange(m), row[b] + np.arange(n_q), [x[b, 0] for x in vecs], n, False)).cuda()
+        for hk in (0, 7):
+            check_sequence(cache, b, hk, m, q[b, :, hk * G:hk * G + G], o[b, :, hk * G:hk * G + G], lse[b, hk * G:hk * G + G],
+                           0.125, ok)
+    empty = torch.from_numpy(lens == 0).cuda()
+    assert (o[empty] == 0).all() and torch.isneginf(lse[empty]).all()
+    none_o, none_lse = fm.fm_cache_attn(cache, q, torch.zeros(B, dtype=torch.int32, device="cuda"), 0.125)
+    assert (none_o == 0).all() and torch.isneginf(none_lse).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_as_many_rows_as_a_call_takes(fm, D):
+    g = torch.Generator(device="cuda").manual_seed(D)
+    cache = shared_page_cache(fm, 1, 1, D, 30, 30, "e4m3", g)
+    q = torch.randn((1, 16, 64, D), generator=g, device="cuda").to(torch.bfloat16)
+    o, lse = fm.fm_cache_attn(cache, q, i32([1900]), 0.1, row=i32([1884]), causal=True)
+    ok = torch.arange(1900, device="cuda") <= 1884 + torch.arange(16, device="cuda")[:, None]
+    check_sequence(cache, 0, 0, 1900, q[0], o[0], lse[0], 0.1, ok)
+
+
+def test_attention_calls_on_two_streams_at_once(fm):
+    """Two calls over one cache that may run at the same time, a workspace each."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    cache = shared_page_cache(fm, 6, 4, 128, 100, 80, "int8", g)
+    q = [torch.randn((6, 1, 16, 128), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2)]
+    n = i32([6400, 1, 3000, 0, 64, 5999])
+    want = [fm.fm_cache_attn(cache, x, n, 0.1) for x in q]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for k in range(2):
+            with torch.cuda.stream(streams[k]):
+                got[k].append(fm.fm_cache_attn(cache, q[k], n, 0.1))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for o, lse in got[k]:
+            assert torch.equal(o, want[k][0]) and torch.equal(lse, want[k][1])
+
+
+def test_what_a_call_allocates_belongs_to_its_stream(fm, monkeypatch):
+    """Workspace and results of a call on a stream that is not the current one come from that stream's memory."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    cache, dst = (shared_page_cache(fm, 2, 2, 64, 4, 8, "int8", g, weight=True) for _ in range(2))
+    dst.page_table.copy_(torch.arange(8, dtype=torch.int32).view(2, 4))
+    q, n = torch.randn((2, 1, 4, 64), generator=g, device="cuda").to(torch.bfloat16), i32([200, 100])
+    want = fm.fm_cache_attn(cache, q, n, 0.1)
+    torch.cuda.synchronize()
+    side, seen = torch.cuda.Stream(), []
+    for name in ("empty", "empty_like"):
+        real = getattr(torch, name)
+        monkeypatch.setattr(torch, name, lambda *a, _real=real, **k: (seen.append(torch.cuda.current_stream()), _real(*a, **k))[1])
+    got = fm.fm_cache_attn(cache, q, n, 0.1, stream=side)
+    fm.fm_cache_evict(cache, dst, n, 64, stream=side)
+    assert len(seen) == 5 and all(x == side for x in seen) and torch.cuda.current_stream() != side
+    side.synchronize()
+    monkeypatch.undo()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_decode_step_captured_and_replayed(fm):
+    """Append, attention with weights and the length's increment in one graph, replayed token by token, against the same
+    calls made one by one: equal bits."""
+    B, H_kv, G, D, steps = 2, 2, 4, 64, 70
+    r = np.random.default_rng(1)
+    k, v = (bf16(x)[1] for x in tokens(r, B, steps, H_kv, D, spread=2.0))
+    q = bf16(r.standard_normal((B, steps, H_kv * G, D)))[1]
+
+    def run(graphed):
+        cache = fm.fm_cache_alloc(B, H_kv, D, 128)
+        ks, vs, qs = (torch.zeros_like(x[:, :1]).contiguous() for x in (k, v, q))
+        at, n = torch.tensor([0, 7], dtype=torch.int32, device="cuda"), torch.tensor([1, 8], dtype=torch.int32, device="cuda")
+        o, lse = torch.empty_like(qs), torch.empty((B, H_kv * G, 1), device="cuda")
+        ws = torch.empty(fm.fm_cache_attn_workspace_bytes(cache, qs, accumulate=True), dtype=torch.uint8, device="cuda")
+        outs = []
+
+        def step():
+            fm.fm_cache_append(cache, ks, vs, at)
+            fm.fm_cache_attn(cache, qs, n, 0.125, row=at, causal=True, accumulate=True, o=o, lse=lse, ws=ws)
+            at.add_(1)
+            n.add_(1)
+        graph = None
+        for t in range(steps):
+            for dst, src in ((ks, k), (vs, v), (qs, q)):
+                dst.copy_(src[:, t:t + 1])
+            if graphed and t == 1:
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph):
+                    step()
+            if graph is None:
+                step()
+            else:
+                graph.replay()
+            outs.append((o.clone(), lse.clone()))
+        torch.cuda.synchronize()
+        return outs, cache
+    a, ca = run(False)
+    b, cb = run(True)
+    for (o1, l1), (o2, l2) in zip(a, b):
+        assert torch.equal(o1, o2) and torch.equal(l1, l2)
+    assert torch.equal(ca.k_codes, cb.k_codes) and torch.equal(ca.v_scale, cb.v_scale) and torch.equal(ca.weight, cb.weight)
+    # every step hands out one unit of weight per query head: a weight is exp(s - lse), off by the relative error of both
+    # exponents (delta each, as above) and of at most 77 additions and as many into the cache
+    mag = 0.125 * q.float().abs().sum(-1).max() * k.float().abs().max() * (1 + 2.0 ** -6)
+    units, delta = steps * B * H_kv * G, (D + 8) * 2.0 ** -23 * mag + 2.0 ** -20
+    assert abs(float(ca.weight.double().sum()) - units) <= units * (2 * delta + 200 * 2.0 ** -24)
+    assert fm.fm_get_device_status() == 0
+
+
 # --------------------------------------------------------------------------------------------- key weight
 def prompt(fm, B, n_q, n_k, H, H_kv, D, vecs, seed):
     r = np.random.default_rng(seed)
@@ -558,6 +723,38 @@ def test_evict_within_one_pool(fm):
     got = dst.k_codes[table.long()].double().cpu().numpy()  # [B, 2, H_kv, 64, D]
     np.testing.assert_array_equal(got.transpose(0, 2, 1, 3, 4), d.units["k"])
     np.testing.assert_array_equal(dst.weight.double().cpu().numpy(), d.weight)
+
+
+@pytest.mark.parametrize("B,H_kv,max_pages", [(64, 4, 800), (1, 2, 6200), (3, 5, 300)])
+def test_evict_long_lists(fm, B, H_kv, max_pages):
+    """Selections whose keys do not fit a CTA's shared memory, that a cluster shares, and in between, against a stable sort."""
+    g = torch.Generator(device="cuda").manual_seed(B)
+    src = shared_page_cache(fm, B, H_kv, 64, max_pages, 12, "int8", g, weight=True)
+    src.weight.copy_(torch.floor(src.weight * 5000) / 5000)  # many ties
+    cap, budget, recent = max_pages * PAGE, max_pages * PAGE // 5 + 3, 77
+    lens = torch.randint(cap // 2, cap + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+    lens[0] = cap
+    dst_pages = -(-budget // PAGE)
+    dst = fm.KVCache(*(torch.zeros((B * dst_pages, H_kv, PAGE, 64), dtype=torch.int8, device="cuda") for _ in range(2)),
+                     *(torch.zeros((B * dst_pages, H_kv), device="cuda") for _ in range(2)),
+                     torch.arange(B * dst_pages, dtype=torch.int32, device="cuda").view(B, dst_pages),
+                     weight=torch.zeros((B, H_kv, dst_pages * PAGE), device="cuda"),
+                     pos=torch.zeros((B, H_kv, dst_pages * PAGE), dtype=torch.int32, device="cuda"))
+    new_len = fm.fm_cache_evict(src, dst, lens, budget, recent=recent)
+    assert (new_len == budget).all() and fm.fm_get_device_status() == 0
+    for b in {0, B // 2, B - 1}:
+        for h in range(H_kv):
+            n = int(lens[b])
+            order = torch.sort(src.weight[b, h, :n - recent], descending=True, stable=True).indices[:budget - recent]
+            kept = torch.cat([order.sort().values, torch.arange(n - recent, n, device="cuda")])
+            assert torch.equal(dst.pos[b, h, :budget].long(), kept)
+            assert torch.equal(dst.weight[b, h, :budget], src.weight[b, h, kept])
+            page = src.page_table[b, kept // PAGE].long()
+            want = src.k_codes[page, h, kept % PAGE].double() * src.k_scale[page, h].double()[:, None]
+            to = torch.arange(budget, device="cuda")
+            got = dst.k_codes[b * dst_pages + to // PAGE, h, to % PAGE].double() * dst.k_scale[b * dst_pages + to // PAGE, h].double()[:, None]
+            step = dst.k_scale[b * dst_pages + to // PAGE, h].double()[:, None]
+            assert ((got - want).abs() <= step / 2).all()  # one rounding of an int8 code
 
 
 # ------------------------------------------------------------------------------------- a run of them together

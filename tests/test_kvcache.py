@@ -33,7 +33,7 @@ def cache_c(**kw):
 BAD_CACHES = [(dict(B=0), 1), (dict(H_kv=0), 1), (dict(n_pages=0), 1), (dict(max_pages=-1), 1), (dict(D=96), 2),
               (dict(code_type=2), 2), (dict(B=65536), 2), (dict(k_codes=None), 1), (dict(v_codes=0x20008), 1),
               (dict(k_scale=None), 1), (dict(page_table=0x50002), 1), (dict(weight=0x60001), 1), (dict(v_scale=0x3), 1),
-              (dict(n_pages=1 << 25), 2), (dict(max_pages=1 << 24), 2)]
+              (dict(n_pages=1 << 25), 2), (dict(max_pages=1 << 24), 2), (dict(max_pages=1 << 22), 2)]
 
 
 @pytest.mark.parametrize("bad,code", BAD_CACHES)
