@@ -669,6 +669,50 @@ def test_key_weight_rows_that_see_nothing(fm):
     assert abs(float(w.double().sum()) - 2 * 160) < 1e-2
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("H,H_kv,Hm_all", [(8, 8, True), (12, 6, False)])
+def test_key_weight_more_key_tiles_than_sms(fm, D, H, H_kv, Hm_all):
+    """Several key tiles a CTA: long lists, short ones, empty ones and whole sequences of empty ones, one after the other."""
+    B, n_q, n_k = 2, 700, 2500
+    r = np.random.default_rng(D + H)
+    vecs = [np.array(x) for x in mask_vectors("window", n_k, B, H if Hm_all else 1, r)]
+    for x, fill in zip(vecs, (0, 1 << 30, 0, 0)):
+        x[:, :, 640:1300] = fill                     # key tiles that no row sees
+        x[0, 0, :] = fill                            # a head, or a whole sequence, that sees nothing
+    for x, fill in zip(vecs, (n_q, n_q, 0, 0)):
+        x[:, -1, 1300:1900] = fill                   # key tiles that every row sees
+    qd, q, kd, k, vt, meta, lse = prompt(fm, B, n_q, n_k, H, H_kv, D, vecs, seed=n_k)
+    scale = 1 / math.sqrt(D)
+    w = fm.fm_attn_key_weight(q, k, lse, meta, vt, scale)
+    check_key_weight(qd, kd, vecs, lse, w.double().cpu().numpy(), scale)
+    # two at once, and replayed from a graph: the same bits
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for x in streams:
+            with torch.cuda.stream(x):
+                got.append(fm.fm_attn_key_weight(q, k, lse, meta, vt, scale))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, w) for x in got)
+    out, graph = torch.zeros_like(w), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fm.fm_attn_key_weight(q, k, lse, meta, vt, scale, weight=out, accumulate=True)
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, 2 * w) and fm.fm_get_device_status() == 0
+
+
+def test_key_weight_nan_rows_reach_the_keys_they_see(fm):
+    n, window = 300, 40
+    vecs = mask_vectors("window", n, 1, 1, None)
+    qd, q, kd, k, vt, meta, lse = prompt(fm, 1, n, n, 2, 1, 64, vecs, seed=3)
+    lse[0, 1, 150] = float("nan")
+    w = fm.fm_attn_key_weight(q, k, lse, meta, vt, 0.125)
+    j = torch.arange(n, device="cuda")
+    assert torch.equal(torch.isnan(w[0, 0]), (j > 150 - window) & (j <= 150))
+
+
 # -------------------------------------------------------------------------------------------------- evict
 @pytest.mark.parametrize("code", ["int8", "e4m3"])
 @pytest.mark.parametrize("D", [64, 128, 256])
