@@ -260,6 +260,7 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 constexpr int kDigitBits = 11;      // a pass
 constexpr int kBins = 1 << kDigitBits;
 constexpr int kSelMaxKeys = 49152;  // keys a CTA can hold in shared memory
+constexpr int kMaxCluster = 8;      // CTAs of a cluster (a power of two of them)
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -442,14 +443,20 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
       constexpr int kQuads = kBins / 4;
       const int quad = kQuads - 1 - (int)threadIdx.x;
       uint32_t t[4] = {0, 0, 0, 0};
-      if (quad >= 0)
-        for (int c = 0; c < size; ++c) {
-          const uint4 v = ld_cluster4(hist + 4 * quad, c);
-          t[0] += v.w;
-          t[1] += v.z;
-          t[2] += v.y;
-          t[3] += v.x;
+      if (quad >= 0) {
+        // the CTAs' counts all in flight at once, each CTA beginning at another one
+        uint4 v[kMaxCluster];
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c)
+          v[c] = c < size ? ld_cluster4(hist + 4 * quad, (rank + c) & (size - 1)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+          t[0] += v[c].w;
+          t[1] += v[c].z;
+          t[2] += v[c].y;
+          t[3] += v[c].x;
         }
+      }
       const uint32_t own = t[0] + t[1] + t[2] + t[3];
       uint32_t x = own;
 #pragma unroll
@@ -733,10 +740,14 @@ fm_status fm_cache_evict(const fm_kv_cache* src, const fm_kv_cache* dst, const i
   p.budget = budget;
   p.recent = recent;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  // The CTAs of a selection: one per 4096 slots of the table, as far as a cluster goes and the SMs are not full yet.
+  // The CTAs of a selection: one per 4096 slots of the table, as far as a cluster goes and all clusters run at once.
   const int64_t slots = (int64_t)src->max_pages * fm::kPage, lists = (int64_t)src->B * src->H_kv;
-  int cluster = 1;
-  while (cluster < 8 && slots > 4096 * (int64_t)cluster && lists * cluster * 2 <= 2 * 148) cluster *= 2;
+  constexpr int kHeldBytes = fm::kSelMaxKeys * 4;
+  if (!fm::smem_opt_in<fm::select_kernel<true, 1024>>(kHeldBytes)) return FM_ERR_CUDA;
+  int cluster = fm::kMaxCluster;
+  while (cluster > 1 && (slots <= 2048 * (int64_t)cluster ||
+                         lists > fm::clusters_at_once<fm::select_kernel<true, 1024>>(cluster, 1024, kHeldBytes)))
+    cluster /= 2;
   p.chunk = (int)(((slots + cluster - 1) / cluster + 31) / 32 * 32);
   const bool held = p.chunk <= fm::kSelMaxKeys;
   // 1024 threads a CTA where there is one CTA per SM at most, 512 where two share one

@@ -1,24 +1,30 @@
 // Attention of a few query rows per sequence over the paged 8-bit K/V cache (fm_cache_attn).
 //
-// The path is bound by the bytes of the cache: every live key's K and V codes are read once, 2 D bytes
-// per key and K/V head, and each is used for the n_q * H / H_kv rows that share the head.  So the design
-// starts from the copies:
+//   O = sum_j p_j v_j / sum_j p_j,   p_j = 2^(s_j - m),   s_j = scale log2(e) (q . code_j) kscale_j,   m >= max_j s_j - 14
+// in one pass over the keys: a running maximum m, the sum of p in fp32, O rescaled whenever m or the block's V scale moves.
+// Bound by the bytes of the cache: every live key's K and V codes are read once, 2 D bytes per key and K/V head, and each is used
+// for the n_q * H / H_kv rows that share the head.  So the design starts from the copies:
 //   * blocks that no row sees are found from the mask vectors by a kernel of its own (only where there is a
 //     mask) before anything of them is loaded; it leaves the list of the others.
 //   * the listed (sequence, K/V head, 64-token block) units of the whole batch form one flat order that is
 //     cut into equal runs, one per CTA (one CTA per SM): ragged lengths, sparse masks and long single
 //     sequences load every SM alike.  A (sequence, head) cut by a run's border is joined by the last kernel.
-//   * each warp owns a ring of K and V blocks in shared memory, filled by TMA (64 rows of D codes, 64- or
+//   * each warp owns a ring of K and V pieces in shared memory, filled by TMA (a piece's keys by up to 128 bytes a box, 64- or
 //     128-byte swizzle) through mbarriers, and works through its share of the run's blocks alone: no CTA
 //     barrier until a (sequence, head) ends.
 // The products run on mma.sync m16n8k16 with fp16 operands and fp32 accumulation, as
 //   S^T [keys x rows] = K Q^T   and   O^T [d x rows] += V^T P^T,
 // so that the 8 columns of the instruction are the few query rows and no row of it is padding for up to
 // 8 rows.  (tcgen05 wants its operands as 16-bit tiles in shared memory or TMEM: converting the codes
-// there and back would move three times the bytes per block that this form does, for a path that needs
-// under a third of mma.sync's rate.)  Both 8-bit formats are exact in fp16, so a score is the exact
+// there and back would move three times the bytes per block that this form does, for a path whose tensor pipe is busy 17% of the
+// time as it is.)  Both 8-bit formats are exact in fp16, so a score is the exact
 // product of q and the cached key, summed in fp32.  The contraction orders are permuted so that a thread's
 // operands are 16 consecutive bytes of a row: over d for K; for V by pairing the bytes of two tokens.
+//
+// Device time (graph of back-to-back calls; D = 128, 8 K/V heads of 4 query heads): one sequence of 131072 tokens 53 us, 5.1 TB/s
+// of codes, of which some 8 us are the start (launch, dependent loads, first copies) and the join; 64 ragged ones of up to 8192
+// with weights 146 us, of which the scores' write and the weights' pass are some 35.  One of 517 tokens (D = 64): 9.8 us, all of
+// it latency.
 #include "fm_cache.cuh"
 
 namespace fm {
@@ -27,7 +33,7 @@ namespace {
 constexpr int kSMs = 148;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-// P is held as 2^14 p in fp16: p down to 2^-28 keeps all 11 bits (half a unit is 2^-12 of p), and 2^14 is
+// P is held as 2^14 p in fp16: p down to 2^-28 keeps all 11 bits (a rounding is at most 2^-11 of p), and 2^14 is
 // exact, so a row that sees one key returns its value unrounded.
 constexpr float kPBias = 14.f;
 
@@ -62,10 +68,11 @@ struct CacheAttnParams {
 
 template <int D, int NT>
 struct CacheAttnCfg {
-  // a warp's piece of work: a block, or half a one where a block's operands would leave the SM too few warps
-  static constexpr int kKeys = D == 256 && NT == 1 ? kPage / 2 : kPage;
+  // a warp's piece of work: a block, or at D = 256 half a one, since a ring of whole ones would leave shared memory for half the
+  // warps (16 sequences of 16384 tokens under a window of 4096, 4 rows: 38 us against 42)
+  static constexpr int kKeys = D == 256 ? kPage / 2 : kPage;
   static constexpr int kParts = kPage / kKeys;
-  static constexpr int kWarps = D == 256 && NT > 1 ? 4 : 8;
+  static constexpr int kWarps = 8;
   static constexpr int kThreads = kWarps * 32;
   // ring slots of a warp (each one K or one V block): what shared memory holds
   static constexpr int kSlots = D == 64 ? 4 : 2;
@@ -150,10 +157,12 @@ __device__ __forceinline__ bool key_seen(const CacheAttnParams& p, const KeyBoun
 
 // Units of a run: an equal share of all, but no fewer than fill the CTA's warps once (that takes no longer than one unit, and
 // leaves fewer partial sums to join) or than an equal cut of the average (sequence, head) into such pieces (short ones each
-// get a CTA of their own: a CTA takes those it holds one after the other).
+// get a CTA of their own: a CTA takes those it holds one after the other).  For the same reason the average itself where that is
+// at most one turn of the warps more (16 sequences of 1000 tokens, 8 K/V heads: 14 us, with equal shares 18).
 __device__ __forceinline__ int units_per_run(const CacheAttnParams& p, int total) {
   const int average = total / (p.B * p.H_kv), pieces = max((average + p.run_min - 1) / p.run_min, 1);
-  return max(max((total + p.n_work - 1) / p.n_work, (average + pieces - 1) / pieces), 1);
+  const int share = max(max((total + p.n_work - 1) / p.n_work, (average + pieces - 1) / pieces), 1);
+  return share < average && average <= share + p.run_min && p.B * p.H_kv * 2 > p.n_work ? average : share;
 }
 
 // How many of the rows [i0, i1) see the key: those not before its pos (causal), less the union of its two stretches.
@@ -185,7 +194,10 @@ __device__ __forceinline__ int2 find_unit(const CacheAttnParams& p, const int* b
 }
 
 // First kernel of a call with a mask: a CTA classifies one chunk of a (sequence, head)'s blocks and lists those that some row
-// sees.  A warp takes kGang blocks at a time (their loads in flight together), two keys per lane.
+// sees.  Per key, a row i0 + t sees it unless t lies in one of two intervals, so the number of rows that see it is interval
+// arithmetic whatever n_q; a block is listed where some key's is above 0, and its mask is left out later where all are n_q.  A
+// warp takes kGang blocks at a time (their loads in flight together), two keys per lane: 20 bytes a key (pos, four bounds),
+// against 2 D of codes, but three dependent loads: latency is what it costs, some 9 us of the call for 16 x 16384 slots x 4 heads.
 constexpr int kPlanThreads = 256;
 constexpr int kMaxChunk = 1024;
 __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const CacheAttnParams p) {
@@ -813,7 +825,11 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
 }
 
 // Last kernel (it may be resident before the one before ends, so what that wrote is read through L2).  The first CTAs join
-// the rows of the (sequence, head)s that several runs share, a CTA per row; the others add the softmax weights of kWeightSlots keys each to the cache's, from the stored scores.
+// the rows of the (sequence, head)s that several runs share, a CTA per row: with M the largest of the runs' maxima,
+// l = sum_c l_c 2^(m_c - M), O = sum_c O_c 2^(m_c - M) / l.  The others add the softmax weights 2^(s - M) / l of kWeightSlots keys
+// each to the cache's, from the stored scores: 4 bytes per key and row written and read (for 4 rows 32 bytes beside a key's 256 of codes), against
+// reading K again and forming its products twice.  1024 slots a CTA, 8 a thread: 64 ragged sequences of up to 8192 tokens, 8 K/V
+// heads: 146 us for the call; 512 slots: 150; 2048: 4 sequences of 2048 take 15.0 us instead of 13.7.
 constexpr int kJoinThreads = 128;
 constexpr int kWeightSlots = 1024;
 constexpr int kMaxRows = 1024;
@@ -951,11 +967,16 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const CacheAtt
 }
 
 // ------------------------------------------------------------------------------------------- host
-// Query rows a CTA holds: 8 for up to 8 rows, more where that spares reading the cache again (through L2)
-// for the next rows, as far as the accumulators fit the registers.
-int row_tiles(int D, int n_rows) {
-  const int most = D == 64 ? 4 : 2;
+// Tiles of 8 query rows that a CTA holds.  More than one spares reading (through L2) and decoding the cache again for the next
+// rows, as far as the accumulators fit the registers: 32 sequences of 8192 tokens, 4 K/V heads, D = 128, 16 rows: 69 us with two
+// tiles, 90 with one; D = 64, 32 rows: 78 us with four, 86 with two, 126 with one.  At D = 256 two tiles leave room for half the
+// warps, which costs what they spare (16 rows: 92 us either way).  Where the table is so small that the rows' CTAs all
+// end after one turn of their warps, a tile each: 500 tokens, 8 K/V heads, D = 128, 16 rows: 10.8 us against 12.3; D = 64, 32
+// rows: 9.8 against 13.4.
+int row_tiles(const fm_kv_cache* c, int n_rows) {
   const int need = (n_rows + 7) / 8;
+  if (c->D == 256 || (int64_t)c->B * c->H_kv * c->max_pages * need <= kSMs * 8) return 1;
+  const int most = c->D == 64 ? 4 : 2;
   return need >= most ? most : need == 3 ? 4 : need;
 }
 
@@ -969,7 +990,7 @@ Layout layout_of(const fm_kv_cache* c, const fm_cache_attn_args* a) {
   Layout L;
   const size_t bh = (size_t)c->B * c->H_kv;
   L.n_rows = a->n_q * (a->H / c->H_kv);
-  L.nt = row_tiles(c->D, L.n_rows);
+  L.nt = row_tiles(c, L.n_rows);
   L.n_row_chunks = (L.n_rows + 8 * L.nt - 1) / (8 * L.nt);
   L.n_rows_pad = L.n_row_chunks * 8 * L.nt;
   L.rows4 = (L.n_rows + 3) / 4 * 4;
@@ -1052,11 +1073,13 @@ fm_status launch(const fm_kv_cache* c, CacheAttnParams p, cudaStream_t s) {
 
 template <int D, bool E4M3>
 fm_status launch_nt(int nt, const fm_kv_cache* c, const CacheAttnParams& p, cudaStream_t s) {
-  if (nt == 1) return launch<D, 1, E4M3>(c, p, s);
   if constexpr (D == 64) {
     if (nt == 4) return launch<D, 4, E4M3>(c, p, s);
   }
-  return launch<D, 2, E4M3>(c, p, s);
+  if constexpr (D < 256) {
+    if (nt == 2) return launch<D, 2, E4M3>(c, p, s);
+  }
+  return launch<D, 1, E4M3>(c, p, s);
 }
 
 }  // namespace

@@ -612,5 +612,27 @@ struct EarlyLaunch {
     attrs[1].val.clusterDim.z = 1;
   }
 };
+// Clusters of `cluster` (2, 4 or 8) CTAs of a kernel that the current device holds at once (a cluster lies within a group of SMs,
+// so of 148 SMs not all can take part: 15 clusters of 8, 33 of 4, 74 of 2 with a CTA per SM).  Asked once per device.
+template <auto kernel>
+int clusters_at_once(int cluster, int threads, int smem_bytes) {
+  static std::atomic<int> known[64][3];  // 1 + the number; 0: not asked yet
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::atomic<int>& n = known[dev][cluster == 2 ? 0 : cluster == 4 ? 1 : 2];
+  if (n.load(std::memory_order_relaxed) == 0) {
+    EarlyLaunch launch(nullptr, cluster);
+    launch.cfg.gridDim = dim3(cluster);
+    launch.cfg.blockDim = dim3(threads);
+    launch.cfg.dynamicSmemBytes = smem_bytes;
+    int fit = 0;
+    if (cudaOccupancyMaxActiveClusters(&fit, kernel, &launch.cfg) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    n.store(1 + fit, std::memory_order_relaxed);
+  }
+  return n.load(std::memory_order_relaxed) - 1;
+}
 bool encode_tmap_u8_rows(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_rows);
 }  // namespace fm

@@ -542,9 +542,10 @@ fm_status launch_key_weight(const fm_attn_args* a, const KeyWeightParams& p, int
       !encode_tmap_bf16_4d(&tk, a->k, D, H_kv, a->n_k, a->B, kTile))
     return FM_ERR_CUDA;
   if (!smem_opt_in<key_weight_kernel<D>>(S::kAlloc)) return FM_ERR_CUDA;
-  // A key tile's query tiles are shared by a cluster of CTAs where there are too few key tiles for the SMs.
-  int cluster = 1;
-  while (cluster < 8 && (int64_t)p.n_work * cluster * 2 <= kSMs) cluster *= 2;
+  // A key tile's query tiles are shared by a cluster of CTAs where there are too few key tiles for the SMs: the largest of
+  // which all run at once.
+  int cluster = 8;
+  while (cluster > 1 && p.n_work > clusters_at_once<key_weight_kernel<D>>(cluster, kThreads, S::kAlloc)) cluster /= 2;
   EarlyLaunch launch(stream, cluster);
   cudaLaunchConfig_t& cfg = launch.cfg;
   cfg.gridDim = dim3((unsigned)(cluster > 1 ? p.n_work * cluster : p.n_work < kSMs ? p.n_work : kSMs));
