@@ -155,13 +155,16 @@ __device__ __forceinline__ bool key_seen(const CacheAttnParams& p, const KeyBoun
   return k.in && !(p.causal && k.j > i) && !(k.lts <= i && i < k.lte) && !(k.uts <= i && i < k.ute);
 }
 
-// Units of a run: an equal share of all, but no fewer than fill the CTA's warps once (that takes no longer than one unit, and
-// leaves fewer partial sums to join) or than an equal cut of the average (sequence, head) into such pieces (short ones each
-// get a CTA of their own: a CTA takes those it holds one after the other).  For the same reason the average itself where that is
-// at most one turn of the warps more (16 sequences of 1000 tokens, 8 K/V heads: 14 us, with equal shares 18).
+// Units of a run: an equal share of all, but no fewer than an equal cut of the average (sequence, head) into pieces of a turn of
+// the CTA's warps (a run of less than a turn takes as long as one unit and leaves more partial sums to join, and a CTA takes
+// the (sequence, head)s it holds one after the other); beyond a turn in whole ones (a part of one takes as long, and borders fall on
+// sequences' ends more often: one sequence of 16384 tokens, 8 K/V heads: 14.7 us, with the bare share 17.3; 8 of 4000: 23.6
+// and 22.3); or the average itself where that is at most one turn more (16 sequences of 1000 tokens, 8 K/V heads: 14 us, with
+// equal shares 18).
 __device__ __forceinline__ int units_per_run(const CacheAttnParams& p, int total) {
   const int average = total / (p.B * p.H_kv), pieces = max((average + p.run_min - 1) / p.run_min, 1);
-  const int share = max(max((total + p.n_work - 1) / p.n_work, (average + pieces - 1) / pieces), 1);
+  int share = max(max((total + p.n_work - 1) / p.n_work, (average + pieces - 1) / pieces), 1);
+  if (share > p.run_min) share = (share + p.run_min - 1) / p.run_min * p.run_min;
   return share < average && average <= share + p.run_min && p.B * p.H_kv * 2 > p.n_work ? average : share;
 }
 
