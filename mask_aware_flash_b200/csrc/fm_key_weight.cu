@@ -9,10 +9,14 @@
 // bits per 32 queries.  One CTA per SM works through a fixed share of the key tiles, longest lists first, and the
 // copies and products of the next key tile start while the last one is still being summed.  Where there are too few
 // key tiles for the SMs a cluster of CTAs shares each one's query tiles and adds up through distributed shared memory.
-// Per score there is one exponential against 2 D flops of the tensor core: for D = 128 the MUFU unit takes 1024 clocks for
-// a tile's 16384 (16 a clock) against 512 of the product.
-// Four warpgroups take the query tiles in turn (so that one's waits hide behind the others' exponentials); one warp lists
-// the items for everybody, some key tiles ahead, one issues the TMA loads, one the MMAs.
+// Bound by the exponentials: per score there is one against 2 D flops of the tensor core, and for D = 128 the MUFU unit takes 1024
+// clocks for a tile's 16384 (16 a clock) against 512 of the product.  8192 tokens in documents, 16 heads, D = 128: 51 us, 7888
+// tiles, 0.59 of that rate; the rest are a tile's other instructions (TMEM loads, multiply-adds and additions share the issue
+// slots with them: without the exponentials it takes 37 us, without the products too 25) and the ends of 1024 uneven lists.
+// 2 x 3996 tokens, 16 heads, D = 64: 53 us, the same unit.  1024 tokens, 8 heads: 13 us, latency (launch, lists, one or two tiles
+// a warpgroup, the cluster's sum).
+// Four warpgroups take the query tiles in turn (so that one's waits hide behind the others' exponentials; three: slower); one
+// warp lists the items for everybody, some key tiles ahead, one issues the TMA loads, one the MMAs.
 #include "fm_common.cuh"
 
 namespace fm {
@@ -543,7 +547,8 @@ fm_status launch_key_weight(const fm_attn_args* a, const KeyWeightParams& p, int
     return FM_ERR_CUDA;
   if (!smem_opt_in<key_weight_kernel<D>>(S::kAlloc)) return FM_ERR_CUDA;
   // A key tile's query tiles are shared by a cluster of CTAs where there are too few key tiles for the SMs: the largest of
-  // which all run at once.
+  // which all run at once.  (1024 tokens, 2 K/V heads: 16 clusters of 4 CTAs 12.9 us, of 8, of which 15 run at once, 16.9, a CTA
+  // each 29.3; 512 tokens: 9.1 with 8, 10.4 with 4, 17.1 with one.)
   int cluster = 8;
   while (cluster > 1 && p.n_work > clusters_at_once<key_weight_kernel<D>>(cluster, kThreads, S::kAlloc)) cluster /= 2;
   EarlyLaunch launch(stream, cluster);
