@@ -34,6 +34,7 @@ CACHE_PAGE = 64  # slots of a page, and tokens that share a scale
 _CODE_TYPES = {torch.int8: 0, torch.float8_e4m3fn: 1}
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 _NO_VECS = VecArray(None, None, None, None)
+_VEC_NAMES = ("vecs[0]", "vecs[1]", "vecs[2]", "vecs[3]")
 
 
 def _lib():
@@ -161,7 +162,7 @@ def _attn_args(what, cache, q, cache_len, scale, row, vecs, causal, accumulate):
             Hm, n_k = ref.shape[1], ref.shape[2]
             for c in range(4):
                 if vecs[c] is not None:
-                    _expect(what, cache.device, f"vecs[{c}]", vecs[c], torch.int32, (cache.B, Hm, n_k))
+                    _expect(what, cache.device, _VEC_NAMES[c], vecs[c], torch.int32, (cache.B, Hm, n_k))
             vec = _vecs(vecs)
     return CacheAttnArgs(q.shape[2], q.shape[1], 0, scale, q.data_ptr(), _ptr(cache_len), _ptr(row), vec, Hm, n_k,
                          1 if causal else 0, 1 if accumulate else 0)
@@ -217,28 +218,39 @@ def fm_attn_key_weight(q, k, lse, meta: MaskMeta, vecs, scale, weight=None, accu
     fm_attn_fwd left or took them.  weight: fp32 [B, H_kv, >= n_k] (a cache's weight; allocated [B, H_kv, n_k] when None),
     written over, or added to with accumulate."""
     what = "fm_attn_key_weight"
-    if q.dim() != 4 or k.dim() != 4 or q.dtype != torch.bfloat16:
+    if q.dim() != 4 or k.dim() != 4 or q.dtype is not torch.bfloat16:
         raise FmError(FM_ERR_INVALID_ARG, f"{what}: q and k must be bfloat16 [B, n, heads, D]")
-    B, n_q, H, D = q.shape
-    n_k, H_kv = k.shape[1], k.shape[2]
-    if weight is None:
-        if accumulate:
-            raise FmError(FM_ERR_INVALID_ARG, f"{what}: accumulate needs a weight to add to")
-        with _allocating(stream):
-            weight = torch.empty((B, H_kv, n_k), dtype=torch.float32, device=q.device)
-    if weight.dim() != 3 or weight.shape[2] < n_k:
-        raise FmError(FM_ERR_INVALID_ARG, f"{what}: weight must be [B, H_kv, >= n_k]")
-    d, dev = meta.desc, q.device
-    _expect(what, dev, "q", q, torch.bfloat16, q.shape)
+    if not q.is_cuda:
+        raise FmError(FM_ERR_INVALID_ARG, f"{what}: q must be a CUDA tensor")
+    dev, q_shape = q.device, q.shape
+    B, n_q, H, D = q_shape
+    _, n_k, H_kv, _ = k.shape
+    _expect(what, dev, "q", q, torch.bfloat16, q_shape)
     _expect(what, dev, "k", k, torch.bfloat16, (B, n_k, H_kv, D))
     _expect(what, dev, "lse", lse, torch.float32, (B, H, n_q))
-    _expect(what, dev, "weight", weight, torch.float32, (B, H_kv, weight.shape[2]))
-    for c in range(4):
-        if vecs[c] is not None:
-            _expect(what, dev, f"vecs[{c}]", vecs[c], torch.int32, (d.B, d.Hm, d.n_k))
+    if weight is not None:
+        if weight.dim() != 3 or weight.shape[2] < n_k:
+            raise FmError(FM_ERR_INVALID_ARG, f"{what}: weight must be [B, H_kv, >= n_k]")
+        stride = weight.shape[2]
+        _expect(what, dev, "weight", weight, torch.float32, (B, H_kv, stride))
+    elif accumulate:
+        raise FmError(FM_ERR_INVALID_ARG, f"{what}: accumulate needs a weight to add to")
+    d = meta.desc
+    vec_shape, vec = (d.B, d.Hm, d.n_k), VecArray()
+    for c, x in enumerate(vecs):
+        if x is not None:
+            _expect(what, dev, _VEC_NAMES[c], x, torch.int32, vec_shape)
+            vec[c] = x.data_ptr()
+    if weight is None:
+        stride = n_k
+        if stream is None:
+            weight = torch.empty((B, H_kv, n_k), dtype=torch.float32, device=dev)
+        else:
+            with _allocating(stream):
+                weight = torch.empty((B, H_kv, n_k), dtype=torch.float32, device=dev)
     a = AttnArgs(B, H, n_q, n_k, D, 0, scale, q.data_ptr(), k.data_ptr(), None, H_kv, 0)
-    _call(_lib().fm_attn_key_weight, what, q.device, stream, ctypes.byref(a), ctypes.byref(meta.c), _vecs(vecs),
-          lse.data_ptr(), weight.data_ptr(), weight.shape[2], 1 if accumulate else 0)
+    _call(_lib().fm_attn_key_weight, what, dev, stream, ctypes.byref(a), ctypes.byref(meta.c), vec, lse.data_ptr(),
+          weight.data_ptr(), stride, 1 if accumulate else 0)
     return weight
 
 

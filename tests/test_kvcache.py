@@ -242,6 +242,9 @@ def test_key_weight_binding(rec):
             fm.fm_attn_key_weight(q, k, lse, m, vecs, 0.1, stream=STREAM, **bad)
     with pytest.raises(fm.FmError):
         fm.fm_attn_key_weight(q, FakeCuda((2, 512, 2, 64), torch.bfloat16), lse, m, vecs, 0.1, weight=w, stream=STREAM)
+    with pytest.raises(fm.FmError):  # host tensors, all of them
+        host = [torch.zeros(x.shape, dtype=x.dtype) for x in (q, k, lse)]
+        fm.fm_attn_key_weight(*host, m, [torch.zeros((2, 1, 512), dtype=torch.int32)] + [None] * 3, 0.1, stream=STREAM)
     assert rec.calls == ["fm_attn_key_weight"]
 
 
