@@ -831,10 +831,13 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
 // the rows of the (sequence, head)s that several runs share, a CTA per row: with M the largest of the runs' maxima,
 // l = sum_c l_c 2^(m_c - M), O = sum_c O_c 2^(m_c - M) / l.  The others add the softmax weights 2^(s - M) / l of kWeightSlots keys
 // each to the cache's, from the stored scores: 4 bytes per key and row written and read (for 4 rows 32 bytes beside a key's 256 of codes), against
-// reading K again and forming its products twice.  1024 slots a CTA, 8 a thread: 64 ragged sequences of up to 8192 tokens, 8 K/V
-// heads: 146 us for the call; 512 slots: 150; 2048: 4 sequences of 2048 take 15.0 us instead of 13.7.
+// reading K again and forming its products twice.  1024 slots a CTA, 8 a thread, for up
+// to 8 rows: 64 ragged sequences of up to 8192 tokens, 8 K/V heads, 4 rows: 145 us for the call (five CTAs an SM instead of six:
+// 148); 512 slots: 150; 2048: 4 sequences
+// of 2048 take 15.0 us instead of 13.7.  512 slots and more CTAs on an SM beyond, where a CTA's time is its rows': 21 sequences of
+// up to 19055 tokens, 80 rows: 305 us; with 1024 slots 347.
 constexpr int kJoinThreads = 128;
-constexpr int kWeightSlots = 1024;
+constexpr int weight_slots(int n_rows) { return n_rows <= 8 ? 1024 : 512; }
 constexpr int kMaxRows = 1024;
 
 struct Span {  // the runs that hold a (sequence, head), and where their partial sums are
@@ -888,8 +891,8 @@ __device__ __forceinline__ float2 join_ml_few(const CacheAttnParams& p, const Sp
   return make_float2(m, l);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const CacheAttnParams p) {
+template <int D, int kWeightSlots>
+__global__ void __launch_bounds__(kJoinThreads, kWeightSlots == 512 ? 8 : 6) cache_join_kernel(const CacheAttnParams p) {
   __shared__ float2 ml[kMaxRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_wait();
@@ -961,7 +964,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const CacheAtt
     v[i] = live[i] ? __ldcg(sc + i * kJoinThreads * p.rows4 / 4) : make_float4(kNegInf, kNegInf, kNegInf, kNegInf);
   }
   // a warp per row, or where there are more rows than warps and few runs a thread per row, their loads in flight together (80 rows
-  // over 21 sequences of up to 19055 tokens, 2 K/V heads: 346 us for the call, 369 with a warp per row)
+  // over 21 sequences of up to 19055 tokens, 2 K/V heads: 346 us for the call, 369 with a warp per row, both with 1024 slots a CTA)
   const bool few = p.rows4 > kJoinThreads / 32 && s.last - s.first < 8;
   const int r_step = few ? kJoinThreads : kJoinThreads / 32;
   for (int r = few ? threadIdx.x : warp; r < p.rows4; r += r_step) {
@@ -1091,11 +1094,12 @@ fm_status launch(const fm_kv_cache* c, CacheAttnParams p, cudaStream_t s) {
   if (e != cudaSuccess) return FM_ERR_CUDA;
   const int64_t bh = (int64_t)p.B * p.H_kv;
   int64_t grid = bh * p.n_rows;
-  if (p.accumulate) grid += bh * ((p.max_pages * kPage + kWeightSlots - 1) / kWeightSlots);
+  if (p.accumulate) grid += bh * ((p.max_pages * kPage + weight_slots(p.n_rows) - 1) / weight_slots(p.n_rows));
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  e = cudaLaunchKernelEx(&cfg, cache_join_kernel<D>, p);
+  e = weight_slots(p.n_rows) == 512 ? cudaLaunchKernelEx(&cfg, cache_join_kernel<D, 512>, p)
+                                    : cudaLaunchKernelEx(&cfg, cache_join_kernel<D, 1024>, p);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? FM_OK : FM_ERR_CUDA;
 }
 
