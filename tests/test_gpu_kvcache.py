@@ -801,6 +801,32 @@ def test_evict_long_lists(fm, B, H_kv, max_pages):
             assert ((got - want).abs() <= step / 2).all()  # one rounding of an int8 code
 
 
+@pytest.mark.parametrize("max_pages", [10, 500])
+def test_evict_captured_and_replayed(fm, max_pages):
+    """The lengths in place (new_len is len), new weights before each replay: the same bits as calls made one by one."""
+    g = torch.Generator(device="cuda").manual_seed(max_pages)
+    src = shared_page_cache(fm, 2, 3, 64, max_pages, 9, "e4m3", g, weight=True)
+    budget = max_pages * 16
+    dst = [fm.fm_cache_alloc(2, 3, 64, budget, codes=torch.float8_e4m3fn) for _ in range(2)]
+    lens = i32([max_pages * PAGE, max_pages * 20])
+    ws = torch.empty(fm.fm_cache_evict_workspace_bytes(src, budget), dtype=torch.uint8, device="cuda")
+    n, graph = lens.clone(), torch.cuda.CUDAGraph()
+    fm.fm_cache_evict(src, dst[1], n, budget, recent=9, new_len=n, ws=ws)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        fm.fm_cache_evict(src, dst[1], n, budget, recent=9, new_len=n, ws=ws)
+    for _ in range(3):
+        src.weight.uniform_(generator=g)
+        want = fm.fm_cache_evict(src, dst[0], lens, budget, recent=9)
+        n.copy_(lens)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(n, want) and torch.equal(want, lens.clamp(max=budget))
+        for a, b in zip((dst[0].weight, dst[0].pos, dst[0].k_codes.view(torch.uint8), dst[0].v_scale),
+                        (dst[1].weight, dst[1].pos, dst[1].k_codes.view(torch.uint8), dst[1].v_scale)):
+            assert torch.equal(a, b)
+
+
 # ------------------------------------------------------------------------------------- a run of them together
 @pytest.mark.parametrize("code", ["int8", "e4m3"])
 def test_prompt_evict_decode(fm, code):
