@@ -53,8 +53,8 @@ struct CacheAttnParams {
   int32_t* units;    // [B * H_kv + 1] units before each (sequence, head)
   int32_t* chunk_n;  // [B * H_kv][n_chunk] listed blocks of each chunk of blocks (mask)
   int32_t* listed;   // [B * H_kv][n_chunk][chunk] those blocks, ascending: block << 1 | some row does not see some key (mask)
-  float* part_o;     // [n_work][2][n_rows_pad][D] partial sums of runs that end inside a (sequence, head)
-  float2* part_ml;   // [n_work][2][n_rows_pad] their running maximum (log2) and sum
+  float* part_o;     // [n_work][2][n_rows_pad][D] O over the keys of runs that end inside a (sequence, head)
+  float2* part_ml;   // [n_work][2][n_rows_pad] their running maximum (log2) and sum of p
   float2* whole_ml;  // [B * H_kv][n_rows_pad] the same for (sequence, head)s inside one run (accumulate)
   float* score;      // [B * H_kv][max_pages * 64][rows4] scores in log2 units (accumulate)
   uint8_t* live;     // [B * H_kv][max_pages] block was read (accumulate)
@@ -794,22 +794,28 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, ml_s[w * C::kRows + n].x);
         const float use = mm == kNegInf ? 0.f : mm;
-        float ll = 0.f, y0 = 0.f, y1 = 0.f;
+        float f[kWarps], ll = 0.f, y0 = 0.f, y1 = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
           const float2 v = ml_s[w * C::kRows + n];
-          const float f = ex2(v.x - use), fo = f * uv_s[w];
+          f[w] = ex2(v.x - use);
+          ll += v.y * f[w];
+        }
+        // The division by the sum comes before V's scale: the quotient is an average of codes, and its product with the scale no
+        // larger than the largest value, where 2^14 n times that may be past fp32's range.
+        const float inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);  // (a NaN stays one)
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
           const float* src = join + (w * C::kRegs + (i * NT + nt) * 4 + x) * 32 + lane;
-          ll += v.y * f;
-          y0 = fmaf(src[0], fo, y0);
-          y1 = fmaf(src[64], fo, y1);
+          const float fo = f[w] * inv;
+          y0 = fmaf(src[0] * fo, uv_s[w], y0);
+          y1 = fmaf(src[64] * fo, uv_s[w], y1);
         }
         const int d = i / (C::kBox / 16) * C::kBox + g * (C::kBox / 8) + 2 * (i % (C::kBox / 16));
         if (whole) {
           if (r >= p.n_rows) continue;
           const int h = hk * p.group + r / p.n_q, tq = r % p.n_q;
-          const float inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);  // (a NaN stays one)
-          *reinterpret_cast<uint32_t*>(p.o + (((int64_t)b * p.n_q + tq) * p.H + h) * D + d) = pack_bf16(y0 * inv, y1 * inv);
+          *reinterpret_cast<uint32_t*>(p.o + (((int64_t)b * p.n_q + tq) * p.H + h) * D + d) = pack_bf16(y0, y1);
           if (i == 0 && g == 0) {
             p.lse[((int64_t)b * p.H + h) * p.n_q + tq] = (mm + log2f(ll)) * kLn2;
             if (p.accumulate) p.whole_ml[(int64_t)bh * p.n_rows_pad + r] = make_float2(mm, ll);
@@ -829,7 +835,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
 
 // Last kernel (it may be resident before the one before ends, so what that wrote is read through L2).  The first CTAs join
 // the rows of the (sequence, head)s that several runs share, a CTA per row: with M the largest of the runs' maxima,
-// l = sum_c l_c 2^(m_c - M), O = sum_c O_c 2^(m_c - M) / l.  The others add the softmax weights 2^(s - M) / l of kWeightSlots keys
+// l = sum_c l_c 2^(m_c - M), O = sum_c O_c (l_c 2^(m_c - M) / l), O_c the run's own quotient (of a value's size, so no sum overflows).  The others add the softmax weights 2^(s - M) / l of kWeightSlots keys
 // each to the cache's, from the stored scores: 4 bytes per key and row written and read (for 4 rows 32 bytes beside a key's 256 of codes), against
 // reading K again and forming its products twice.  1024 slots a CTA, 8 a thread, for up
 // to 8 rows: 64 ragged sequences of up to 8192 tokens, 8 K/V heads, 4 rows: 145 us for the call (five CTAs an SM instead of six:
@@ -913,7 +919,8 @@ __global__ void __launch_bounds__(kJoinThreads, kWeightSlots == 512 ? 8 : 6) cac
 #pragma unroll 4
     for (int c = s.first + warp; c <= s.last; c += kJoinThreads / 32) {
       const int64_t at = part_of(p, s, c) + r;
-      const float f = ex2(__ldcg(&p.part_ml[at].x) - use);
+      const float2 ml_c = __ldcg(&p.part_ml[at]);
+      const float f = ml_c.y * ex2(ml_c.x - use) * inv;
       const float2* src = reinterpret_cast<const float2*>(p.part_o + at * D + lane * kPer);
 #pragma unroll
       for (int i = 0; i < kPer; i += 2) {
@@ -934,7 +941,7 @@ __global__ void __launch_bounds__(kJoinThreads, kWeightSlots == 512 ? 8 : 6) cac
         y0 += part[w][2 * d];
         y1 += part[w][2 * d + 1];
       }
-      dst[d] = pack_bf16(y0 * inv, y1 * inv);
+      dst[d] = pack_bf16(y0, y1);
     }
     if (threadIdx.x == 0) p.lse[((int64_t)b * p.H + h) * p.n_q + tq] = t.y == 0.f ? kNegInf : (t.x + log2f(t.y)) * kLn2;
     return;

@@ -354,6 +354,35 @@ def test_attention_one_key_returns_its_value(fm):
         assert torch.equal(o[0, 0, h].cpu(), want)
 
 
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n", [1, 200, 3000])
+def test_attention_of_the_largest_values(fm, D, code, n):
+    """Values at the upper end of fp32: one key seen returns its value, equal keys return theirs, others their average."""
+    big = {"int8": 127 * 2.0 ** 121, "e4m3": 448 * 2.0 ** 119}[code]  # the largest code under the largest scale
+    r = np.random.default_rng(n + D)
+    c = Pair(fm, 1, 1, D, -(-n // PAGE), code)
+    k = r.standard_normal((1, n, 1, D))
+    sign = np.where(r.integers(0, 2, D) > 0, 1.0, -1.0)
+    c.append(fm, k, np.tile(big * sign, (1, n, 1, 1)), [0])
+    qd, q = bf16(r.standard_normal((1, 2, 3, D)))
+    o, _ = run_attention(fm, c, [n], q, 0.1, None, None, False, False)
+    assert fm.fm_get_device_status() == 0
+    assert torch.equal(o.double().cpu(), torch.from_numpy(np.broadcast_to(big * sign, (1, 2, 3, D)).copy()))
+    # every row sees one key only, another one each (row t: key at[t])
+    at = r.integers(0, n, 2)
+    vecs = [np.full((1, 1, n), x, np.int32) for x in (0, 1, 1, 2)]  # both rows masked, each by one stretch
+    vecs[1][0, 0, at[0]] = 0
+    vecs[3][0, 0, at[1]] = 1
+    o, lse = run_attention(fm, c, [n], q, 0.1, np.array([0]), vecs, False, False)
+    assert torch.equal(o.double().cpu(), torch.from_numpy(np.broadcast_to(big * sign, (1, 2, 3, D)).copy()))
+    # values of either sign and of several sizes, the largest 2^126
+    v = r.uniform(-1, 1, (1, n, 1, D)) * np.exp2(126 - r.integers(0, 6, (1, n, 1, 1)))
+    c.append(fm, k, v, [0])
+    o, lse = run_attention(fm, c, [n], q, 0.1, None, None, False, False)
+    check_attention(c, [n], qd, o, lse, 0.1, None, None, False)
+
+
 def test_attention_streams_workspaces_and_graphs(fm):
     """A poisoned workspace, another stream, a captured and replayed call whose inputs change, two graphs that share a
     workspace (replayed one after the other), and equal bits every time."""
