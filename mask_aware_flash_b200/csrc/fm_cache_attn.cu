@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
         bool moved = false;
         float alpha[NT][2];
         const float unit_new = vs > 0.f ? fmaxf(vs, fmaxf(max_v, vs) * 9.094947e-13f) : unit_v;  // 2^-40: see below
-        const float p_scale = unit_new == vs || vs == 0.f ? 1.f : vs / unit_new;
+        const float p_scale = vs == 0.f ? 0.f : unit_new == vs ? 1.f : vs / unit_new;  // (scale 0: values 0, whatever the codes)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll

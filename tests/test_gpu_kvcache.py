@@ -495,6 +495,29 @@ def check_sequence(cache, b, hk, n, q, o, lse, scale, ok=None):
     assert ((got - L)[live].abs() <= (delta + n * 2.0 ** -24 + 2.0 ** -22 * L.abs())[live]).all()
 
 
+@pytest.mark.parametrize("code,D,G", [("int8", 64, 2), ("int8", 64, 11), ("int8", 128, 3), ("e4m3", 128, 5), ("e4m3", 256, 2)])
+@pytest.mark.parametrize("B,H_kv,max_pages", [(24, 4, 30), (1, 1, 1500), (5, 2, 3)])
+def test_attention_zero_scales_over_codes_that_are_not(fm, code, D, G, B, H_kv, max_pages):
+    """A pool of the caller's own may hold any codes under a scale of 0: their values are 0, as keys and as values."""
+    g = torch.Generator(device="cuda").manual_seed(D + G + B)
+    cache = shared_page_cache(fm, B, H_kv, D, max_pages, 90, code, g)
+    cache.v_scale[::3] = 0
+    cache.k_scale[::5] = 0
+    lens = np.random.default_rng(B).integers(max_pages * 30, max_pages * PAGE + 1, B)
+    if B == 5:
+        cache.page_table[1] = 3   # a sequence of such blocks alone, and one that begins, one that ends with them
+        cache.page_table[2, 0] = cache.page_table[3, -1] = 6
+    q = torch.randn((B, 1, H_kv * G, D), generator=g, device="cuda").to(torch.bfloat16)
+    o, lse = fm.fm_cache_attn(cache, q, i32(lens), 0.1)
+    assert fm.fm_get_device_status() == 0
+    for b in range(B) if B == 5 else {0, B // 2, B - 1}:
+        for hk in {0, H_kv - 1}:
+            heads = slice(hk * G, hk * G + G)
+            check_sequence(cache, b, hk, int(lens[b]), q[b, :, heads], o[b, :, heads], lse[b, heads], 0.1)
+    if B == 5:
+        assert (o[1] == 0).all()
+
+
 def test_attention_many_sequences_and_long_masks(fm):
     """More (sequence, head) lists than threads, chunks of more than 64 blocks, masks over several chunks, empty sequences."""
     B, H_kv, G, D, max_pages, n_q = 520, 8, 2, 64, 200, 2
