@@ -368,7 +368,9 @@ size_t fm_cache_attn_workspace_bytes(const fm_kv_cache* cache, const fm_cache_at
 /*
  * For every sequence b, query t and head h, with U the unmasked keys among the first len[b] slots of
  * K/V head h / (H / H_kv):  O = sum_{j in U} softmax_j(scale q.k_j) v_j and
- * LSE = ln sum_{j in U} exp(scale q.k_j); U empty: O = 0, LSE = -inf (as fm_attn_fwd).  Blocks whose
+ * LSE = ln sum_{j in U} exp(scale q.k_j); U empty: O = 0, LSE = -inf (as fm_attn_fwd).  The scores have
+ * to lie in fp32's range.  A key's share of O counts as 0 where its softmax weight is under 2^-110, and
+ * may lose bits where it is under 2^-100 of the row's largest element of O.  Blocks whose
  * keys are masked for every row are not read.  accumulate = 1: weight[b, hk, j] += the sum of key j's
  * softmax weights over the rows of the heads that share hk.  Every sum has a fixed order: the same
  * call gives the same bits.

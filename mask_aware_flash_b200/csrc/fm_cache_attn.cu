@@ -1,7 +1,7 @@
 // Attention of a few query rows per sequence over the paged 8-bit K/V cache (fm_cache_attn).
 //
 //   O = sum_j p_j v_j / sum_j p_j,   p_j = 2^(s_j - m),   s_j = scale log2(e) (q . code_j) kscale_j,   m >= max_j s_j - 14
-// in one pass over the keys: a running maximum m, the sum of p in fp32, O rescaled whenever m or the block's V scale moves.
+// in one pass over the keys: a running maximum m, the sum of p in fp32, O rescaled whenever m or its unit moves.
 // Bound by the bytes of the cache: every live key's K and V codes are read once, 2 D bytes per key and K/V head, and each is used
 // for the n_q * H / H_kv rows that share the head.  So the design starts from the copies:
 //   * blocks that no row sees are found from the mask vectors by a kernel of its own (only where there is a
@@ -36,6 +36,15 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // P is held as 2^14 p in fp16: p down to 2^-28 keeps all 11 bits (a rounding is at most 2^-11 of p), and 2^14 is
 // exact, so a row that sees one key returns its value unrounded.
 constexpr float kPBias = 14.f;
+// That is with O in units of the block's V scale.  In general a row's O is held in units of 2^u, u a whole number of the row's own, and
+// its P is 2^14 p vscale / 2^u.  u stays while the largest P of the row's live keys in a block lies in [1, 2^15.5] (fp16 ends at 65504:
+// p down to 2^-14 of the block's largest keeps all its bits), and otherwise moves so that the largest comes to 2^14: no key's share is
+// lost where V's scales or the softmax weights of two blocks are far apart, in either order, and a block that a row does not see does
+// not matter to it.  O moves with u, in fp32, as far as 2^kORoom; so what a block adds loses bits only where it is under 2^-118 of the
+// largest element of the row's O.  (One unit for all rows, the block's scale, loses rows whose scales are 2^80 under another row's; a
+// unit per row costs 1% at 8 rows, 4% at 32 rows of D = 64: 32 sequences of 8192 tokens 74.6 -> 77.5 us.)
+constexpr float kPMid = 7.75f;  // half of 15.5
+constexpr int kORoom = 118, kUnitMax = 126;
 
 struct CacheAttnParams {
   const __nv_bfloat16* q;
@@ -91,9 +100,8 @@ struct CacheAttnCfg {
   static constexpr int kSegBh = kSegStart + (kCap + 4) * 4;             // int [kCap]
   static constexpr int kSegFlag = kSegBh + kCap * 4;                    // int [kCap]
   static constexpr int kUnitBh = kSegFlag + kCap * 4;                   // int [kCap + 2]: of the units, one before and one behind
-  static constexpr int kMl = kUnitBh + (kCap + 4) * 4;                  // float2 [warps][rows]
-  static constexpr int kUv = kMl + kWarps * kRows * 8;                  // float [warps]: the units of their O
-  static constexpr int kQs = kUv + kWarps * 4;                          // float [rows]
+  static constexpr int kMl = kUnitBh + (kCap + 4) * 4;                  // float4 [warps][rows]: maximum, sum, unit of O
+  static constexpr int kQs = kMl + kWarps * kRows * 16;                 // float [rows]
   static constexpr int kBits = kQs + kRows * 4;                         // uint2 [warps][rows] mask bits
   static constexpr int kBar = kBits + kWarps * kRows * 8;               // mbarriers [warps][slots]
   static constexpr int kMisc = kBar + kWarps * kSlots * 8;              // abort, zero
@@ -101,7 +109,7 @@ struct CacheAttnCfg {
   static constexpr int kBefore = kRed + 128;                            // int [threads]: units before each thread's lists
   static constexpr int kBytes = kBefore + kThreads * 4;
   static constexpr int kAlloc = kBytes + 1024;
-  static_assert(kList % 16 == 0 && kMl % 8 == 0 && kBits % 8 == 0 && kBar % 8 == 0, "shared memory alignment");
+  static_assert(kList % 16 == 0 && kMl % 16 == 0 && kBits % 8 == 0 && kBar % 8 == 0, "shared memory alignment");
 };
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
@@ -129,6 +137,14 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // -126 <= e <= 127
+__device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_uint(x) >> 23 & 255u) - 127; }
 
 // Bounds of one cached key: its row index and its two masked stretches.
 struct KeyBounds {
@@ -276,6 +292,43 @@ constexpr int kBegin = 4;   // its first units at all
 constexpr int kEndAll = 8;  // its last ones
 constexpr int kInside = 16; // kBegin, and not at the run's first unit
 
+// Moves the units of rows whose largest P of this block would be out of range (see kPMid), with their O, and with alpha, which is 1
+// afterwards.  The eight lanes of a row hold other elements of its O and decide alike: all else is the same to them.
+template <int NT, int kTiles>
+__device__ __forceinline__ void move_units(float (&o)[kTiles][NT][4], float (&alpha)[NT][2], const float (&above)[NT][2],
+                                           float (&per_unit)[NT][2], float vs) {
+  const int v_exp = exponent_of(vs);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      float big = 0.f;
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) big = fmaxf(big, fmaxf(fabsf(o[i][nt][x]), fabsf(o[i][nt][2 + x])));
+#pragma unroll
+      for (int y = 4; y < 32; y <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, y));
+      big *= alpha[nt][x];
+      const int u = -exponent_of(per_unit[nt][x]);
+      const float top = above[nt][x] + lg2(fabsf(vs * pow2i(-v_exp))) + (float)(v_exp - u);  // of P
+      int to = u;
+      if (above[nt][x] != kNegInf && fabsf(top - kPMid) > kPMid) {
+        to = u + (int)rintf(top - kPBias);
+        if (big > 0.f) to = max(to, u + exponent_of(big) - kORoom);
+        to = min(max(max(to, v_exp - kUnitMax), -kUnitMax), kUnitMax);  // (vs / 2^u and 2^-u stay finite)
+        per_unit[nt][x] = pow2i(-to);
+      }
+      // in two steps that neither overflow nor lose what the end keeps
+      const int d = u - to, d1 = d / 2;
+      const float f0 = alpha[nt][x] * pow2i(d1), f1 = pow2i(d - d1);
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) {
+        o[i][nt][x] = o[i][nt][x] * f0 * f1;
+        o[i][nt][2 + x] = o[i][nt][2 + x] * f0 * f1;
+      }
+      alpha[nt][x] = 1.f;
+    }
+}
+
 template <int D, int NT, bool E4M3>
 __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -296,8 +349,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
   int* seg_bh = reinterpret_cast<int*>(smem + C::kSegBh);
   int* seg_flag = reinterpret_cast<int*>(smem + C::kSegFlag);
   int* unit_bh = reinterpret_cast<int*>(smem + C::kUnitBh) + 1;  // [-1 .. kCap]
-  float2* ml_s = reinterpret_cast<float2*>(smem + C::kMl);
-  float* uv_s = reinterpret_cast<float*>(smem + C::kUv);
+  float4* ml_s = reinterpret_cast<float4*>(smem + C::kMl);
   float* qs_s = reinterpret_cast<float*>(smem + C::kQs);
   uint2* bits_s = reinterpret_cast<uint2*>(smem + C::kBits) + warp * C::kRows;
   int* misc = reinterpret_cast<int*>(smem + C::kMisc);
@@ -350,7 +402,7 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
     for (int e = threadIdx.x; e <= p.B * p.H_kv; e += kThreads) p.units[e] = 0;
   float o[kTiles][NT][4];
   float m[NT][2], l[NT][2];
-  float unit_v = 0.f, max_v = 0.f;  // O is held in units of unit_v (the V scale of the last block)
+  float per_unit[NT][2];            // 2^-u of the row's unit of O
   int item = 0;                     // ring items consumed by this warp so far
   int begun = 0;                    // flags of the current segment's first units
   bool ok = true;
@@ -528,16 +580,18 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
       const int len = min(max(*(p.len + b), 0), cap);
       if (flag & kReset) {
         begun = flag;
+        const int e = warp + kWarps * (done >> 1);  // the warp's first piece: its scale is the unit to begin with
+        const float start = e < e1 ? pow2i(-min(max(exponent_of(__int_as_float(list[e / C::kParts].w)), -kUnitMax), kUnitMax)) : 1.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           m[nt][0] = m[nt][1] = kNegInf;
           l[nt][0] = l[nt][1] = 0.f;
+          per_unit[nt][0] = per_unit[nt][1] = start;
 #pragma unroll
           for (int i = 0; i < kTiles; ++i)
 #pragma unroll
             for (int c = 0; c < 4; ++c) o[i][nt][c] = 0.f;
         }
-        unit_v = max_v = 0.f;
       }
       for (int e = warp + kWarps * (done >> 1); e < e1; e += kWarps) {
         const int4 ent = list[e / C::kParts];
@@ -633,10 +687,8 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
         ++done;
         // ------------------------------------------------------------ softmax: this thread's rows 2t, 2t+1
         uint32_t pb[kJ][NT][2];  // P^T fragments
-        bool moved = false;
-        float alpha[NT][2];
-        const float unit_new = vs > 0.f ? fmaxf(vs, fmaxf(max_v, vs) * 9.094947e-13f) : unit_v;  // 2^-40: see below
-        const float p_scale = vs == 0.f ? 0.f : unit_new == vs ? 1.f : vs / unit_new;  // (scale 0: values 0, whatever the codes)
+        bool moved = false, far = false;
+        float alpha[NT][2], above[NT][2];  // above: the block's largest score over m (-inf: the row sees no key)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -685,23 +737,27 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
               sum += s[j][nt][x] + s[j][nt][2 + x];
             }
             l[nt][x] = fmaf(l[nt][x], alpha[nt][x], sum);
-          }
-#pragma unroll
-          for (int j = 0; j < kJ; ++j) {  // keys 16 j + 2t, +1 and + 8, + 9 of row g, as the product reads them
-            pb[j][nt][0] = transpose8x8(pack_f16(s[j][nt][0] * p_scale, s[j][nt][1] * p_scale));
-            pb[j][nt][1] = transpose8x8(pack_f16(s[j][nt][2] * p_scale, s[j][nt][3] * p_scale));
+            above[nt][x] = mx - m_use;
+            // log2 of the block's largest P, outside [0, 2 kPMid]?
+            far |= mx != kNegInf && fabsf(above[nt][x] + (lg2(fabsf(vs * per_unit[nt][x])) - kPMid)) > kPMid;
           }
         }
-        // O moves to this block's maximum and V scale.  The V scale is a common factor of a block's codes, so
-        // O is held in units of the last block's; a block more than 2^40 below the largest one seen keeps to
-        // 2^-40 of that, its P scaled instead (O would overflow in ever smaller units).
-        const float fu = unit_v == unit_new || unit_v == 0.f ? 1.f : unit_v / unit_new;
-        max_v = fmaxf(max_v, vs);
-        unit_v = unit_new;
-        if (__any_sync(0xffffffffu, moved || fu != 1.f)) {
+        if (__any_sync(0xffffffffu, far) && vs != 0.f) move_units<NT, kTiles>(o, alpha, above, per_unit, vs);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float pf0 = above[nt][0] != kNegInf ? vs * per_unit[nt][0] : 0.f;  // P / p
+          const float pf1 = above[nt][1] != kNegInf ? vs * per_unit[nt][1] : 0.f;
+#pragma unroll
+          for (int j = 0; j < kJ; ++j) {  // keys 16 j + 2t, +1 and + 8, + 9 of row g, as the product reads them
+            pb[j][nt][0] = transpose8x8(pack_f16(s[j][nt][0] * pf0, s[j][nt][1] * pf1));
+            pb[j][nt][1] = transpose8x8(pack_f16(s[j][nt][2] * pf0, s[j][nt][3] * pf1));
+          }
+        }
+        // O moves to the new maximum
+        if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const float f0 = alpha[nt][0] * fu, f1 = alpha[nt][1] * fu;
+            const float f0 = alpha[nt][0], f1 = alpha[nt][1];
 #pragma unroll
             for (int i = 0; i < kTiles; ++i) {
               o[i][nt][0] *= f0;
@@ -774,14 +830,15 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
         for (int x = 0; x < 2; ++x) {
 #pragma unroll
           for (int y = 4; y < 32; y <<= 1) l[nt][x] += __shfl_xor_sync(0xffffffffu, l[nt][x], y);
-          if (g == 0) ml_s[warp * C::kRows + nt * 8 + 2 * t + x] = make_float2(m[nt][x], l[nt][x]);
+          if (g == 0)
+            ml_s[warp * C::kRows + nt * 8 + 2 * t + x] =
+                make_float4(m[nt][x], l[nt][x], pow2i(-exponent_of(per_unit[nt][x])), 0.f);
         }
 #pragma unroll
         for (int i = 0; i < kTiles; ++i)
 #pragma unroll
           for (int c = 0; c < 4; ++c) join[(warp * C::kRegs + (i * NT + nt) * 4 + c) * 32 + lane] = o[i][nt][c];
       }
-      if (lane == 0) uv_s[warp] = unit_v;
       __syncthreads();
       // each warp adds up a share of the accumulators' places (pairs: the same row, d and d + 1) over the warps, in order
       const bool whole = (begun & kBegin) && (flag & kEndAll);
@@ -794,22 +851,23 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, ml_s[w * C::kRows + n].x);
         const float use = mm == kNegInf ? 0.f : mm;
-        float f[kWarps], ll = 0.f, y0 = 0.f, y1 = 0.f;
+        float f[kWarps], unit[kWarps], ll = 0.f, y0 = 0.f, y1 = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          const float2 v = ml_s[w * C::kRows + n];
+          const float4 v = ml_s[w * C::kRows + n];
           f[w] = ex2(v.x - use);
+          unit[w] = v.z;
           ll += v.y * f[w];
         }
-        // The division by the sum comes before V's scale: the quotient is an average of codes, and its product with the scale no
+        // The division by the sum comes before the unit: the quotient is an average of codes, and its product with the unit no
         // larger than the largest value, where 2^14 n times that may be past fp32's range.
         const float inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);  // (a NaN stays one)
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
           const float* src = join + (w * C::kRegs + (i * NT + nt) * 4 + x) * 32 + lane;
           const float fo = f[w] * inv;
-          y0 = fmaf(src[0] * fo, uv_s[w], y0);
-          y1 = fmaf(src[64] * fo, uv_s[w], y1);
+          y0 = fmaf(src[0] * fo, unit[w], y0);
+          y1 = fmaf(src[64] * fo, unit[w], y1);
         }
         const int d = i / (C::kBox / 16) * C::kBox + g * (C::kBox / 8) + 2 * (i % (C::kBox / 16));
         if (whole) {

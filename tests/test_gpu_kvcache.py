@@ -549,6 +549,64 @@ def test_attention_many_sequences_and_long_masks(fm):
     assert (none_o == 0).all() and torch.isneginf(none_lse).all()
 
 
+def far_apart(fm, kind, code, D, G, B, H_kv, max_pages, seed):
+    """A cache whose pages fall into three classes, in random order along each sequence: cache, class of each block, q, row, vectors."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    n_pages = 90
+    cls = torch.arange(n_pages, device="cuda") % 3
+    codes = [torch.randint(-20, 21, (n_pages, H_kv, PAGE, D), generator=g, device="cuda").float(),
+             torch.randint(-100, 101, (n_pages, H_kv, PAGE, D), generator=g, device="cuda").float()]
+    exps = {"seen": (100, 0, -100), "columns": (45, 0, -45), "weights": (100, 0, 0), "negative": (30, 0, -30)}[kind]
+    scale = [torch.full((n_pages, H_kv), 2.0 ** -7, device="cuda"),
+             torch.exp2(torch.tensor(exps, device="cuda").float())[cls][:, None].repeat(1, H_kv)]
+    q = torch.randn((B, 3, H_kv * G, D), generator=g, device="cuda")
+    if kind == "columns":   # an element of V that only the smaller classes have, another that only the smallest has
+        codes[1][cls == 0, :, :, 5] = 0
+        codes[1][cls <= 1, :, :, 17] = 0
+    if kind == "weights":   # keys of the first class have softmax weights some 2^-45 of the others'
+        codes[0][:, :, :, 0] = torch.where(cls == 0, -100.0, 100.0)[:, None, None]
+        q[..., 0] = 200.0
+    if kind == "negative":  # any scales of a pool of the caller's own: negative ones, and no powers of two
+        scale = [s * (torch.rand(s.shape, generator=g, device="cuda") + 0.999) for s in scale]
+        scale = [torch.where(torch.rand(s.shape, generator=g, device="cuda") < 0.5, s, -s) for s in scale]
+    if code == "e4m3":
+        codes, scale[0] = [x / 16 for x in codes], scale[0] * 16
+    codes = [x.to(CODES[code]) for x in codes]
+    table = torch.randint(0, n_pages, (B, max_pages), generator=g, device="cuda", dtype=torch.int32)
+    row = torch.arange(B, device="cuda", dtype=torch.int32) + 5000
+    vecs = None
+    if kind == "seen":      # query 1 sees none of the first class, query 2 only the third
+        of = cls[table.long()].repeat_interleave(PAGE, 1)[:, None]
+        at = row[:, None, None]
+        zero = torch.zeros_like(of, dtype=torch.int32)
+        vecs = [torch.where(of == 0, at + 1, zero), torch.where(of == 0, at + 3, zero),
+                torch.where(of == 1, at + 2, zero), torch.where(of == 1, at + 3, zero)]
+        vecs = [x.to(torch.int32).contiguous() for x in vecs]
+    return fm.KVCache(*codes, *scale, table), q.to(torch.bfloat16), row, vecs
+
+
+@pytest.mark.parametrize("kind", ["seen", "columns", "weights", "negative"])
+@pytest.mark.parametrize("code,D,G", [("int8", 64, 1), ("int8", 64, 11), ("int8", 128, 1), ("e4m3", 128, 5), ("e4m3", 256, 2)])
+@pytest.mark.parametrize("B,H_kv,max_pages", [(24, 4, 30), (1, 1, 1500)])
+def test_attention_value_scales_and_weights_far_apart(fm, kind, code, D, G, B, H_kv, max_pages):
+    """V scales whose ratios are far beyond fp16's range, several such blocks in the hands of each warp, in every order: rows that do
+    not see the larger ones, elements that these do not have, and large values under small weights keep their bits."""
+    cache, q, row, vecs = far_apart(fm, kind, code, D, G, B, H_kv, max_pages, seed=D + G + B)
+    lens = np.random.default_rng(D + B).integers(max_pages * 30, max_pages * PAGE + 1, B)
+    o, lse = fm.fm_cache_attn(cache, q, i32(lens), 0.1, row=row, vecs=vecs)
+    assert fm.fm_get_device_status() == 0
+    for b in {0, B // 2, B - 1}:
+        n = int(lens[b])
+        ok = None
+        if vecs is not None:
+            i = row[b].long() + torch.arange(3, device="cuda")[:, None]
+            lts, lte, uts, ute = (x[b, 0, None, :n].long() for x in vecs)
+            ok = ~(((lts <= i) & (i < lte)) | ((uts <= i) & (i < ute)))
+        for hk in {0, H_kv - 1}:
+            heads = slice(hk * G, hk * G + G)
+            check_sequence(cache, b, hk, n, q[b, :, heads], o[b, :, heads], lse[b, heads], 0.1, ok)
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_attention_as_many_rows_as_a_call_takes(fm, D):
     g = torch.Generator(device="cuda").manual_seed(D)
