@@ -1100,9 +1100,12 @@ Layout layout_of(const fm_kv_cache* c, const fm_cache_attn_args* a) {
   L.units = take((bh + 1) * 4);
   // chunks of 32 blocks, which a CTA of the plan lists in one go (2 sequences of 34954 tokens under a window per head, 8 heads: 34.5 us
   // for the call, 45.8 with chunks of 64); larger ones where that would make more than 1024 lists, and of 64 than 8192: every CTA of
-  // the main kernel adds up all their lengths
+  // the main kernel adds up all their lengths; none longer than the table
   L.chunk = 32;
-  while (L.chunk < kMaxChunk && bh * ((c->max_pages + L.chunk - 1) / L.chunk) > (L.chunk < 64 ? 1024 : 8192)) L.chunk *= 2;
+  while (L.chunk < kMaxChunk && L.chunk < c->max_pages &&
+         bh * ((c->max_pages + L.chunk - 1) / L.chunk) > (L.chunk < 64 ? 1024 : 8192))
+    L.chunk *= 2;
+  if (L.chunk > c->max_pages) L.chunk = c->max_pages;
   L.n_chunk = (c->max_pages + L.chunk - 1) / L.chunk;
   L.chunk_n = take(bh * L.n_chunk * 4);
   L.listed = take(bh * L.n_chunk * L.chunk * 4);

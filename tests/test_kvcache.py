@@ -98,6 +98,20 @@ def test_attention_workspace(L):
     assert L.fm_cache_attn_workspace_bytes(r(none), r(a)) == 0
 
 
+@pytest.mark.parametrize("D,group,n_q", [(64, 1, 1), (128, 4, 1), (256, 2, 3)])
+@pytest.mark.parametrize("B,H_kv,max_pages", [(1, 1, 1), (1100, 8, 4), (8192, 8, 8), (65535, 8, 16), (33, 1, 31), (3, 2, 5000),
+                                              (300, 8, 33), (64, 8, 2048)])
+def test_attention_workspace_goes_with_the_table(L, D, group, n_q, B, H_kv, max_pages):
+    """Without weights: a word per listed block (two where lists are shorter than their room), a word per (sequence, head) and list, and
+    the partial sums of 148 CTAs."""
+    a = fm.CacheAttnArgs(H=H_kv * group, n_q=n_q, dtype=0, scale=0.1, q=0x100000, len=0x200000)
+    c = cache_c(B=B, H_kv=H_kv, D=D, max_pages=max_pages, n_pages=1 << 16)
+    got = L.fm_cache_attn_workspace_bytes(ctypes.byref(c), ctypes.byref(a))
+    rows = -(-n_q * group // 8) * 8
+    parts = 2 * 148 * rows * (D + 2) * 4
+    assert 0 < got <= B * H_kv * (8 * max_pages + 8) + parts + 8 * 256
+
+
 def test_evict_refusals(L):
     src, dst = cache_c(), cache_c(k_codes=0x110000, v_codes=0x120000, k_scale=0x130000, v_scale=0x140000, page_table=0x150000,
                                   weight=0x160000, pos=0x170000, max_pages=2)
