@@ -71,7 +71,8 @@ def _expect(what, device, name, t, dtype, shape):
 
 
 class KVCache:
-    """The tensors of one layer's cache, checked once.
+    """The tensors of one layer's cache, checked once and fixed: their addresses are taken here, so an attribute set later
+    is refused (make another KVCache for other tensors; what the tensors hold may change at any time).
 
     k_codes, v_codes: int8 or float8_e4m3fn [n_pages, H_kv, 64, D]; k_scale, v_scale: float32 [n_pages, H_kv];
     page_table: int32 [B, max_pages]; weight: float32, pos: int32, both [B, H_kv, max_pages * 64] or None.
@@ -106,6 +107,14 @@ class KVCache:
                           v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), page_table.data_ptr(),
                           None if weight is None else weight.data_ptr(), None if pos is None else pos.data_ptr())
         self._ref = ctypes.byref(self.c)
+
+    def __setattr__(self, name, value):
+        if "_ref" in self.__dict__:
+            raise AttributeError(f"KVCache: {name} cannot be set: calls use the tensors that the cache was made with")
+        object.__setattr__(self, name, value)
+
+    def __delattr__(self, name):
+        raise AttributeError(f"KVCache: {name} cannot be deleted: calls use the tensors that the cache was made with")
 
     @property
     def slots(self) -> int:

@@ -210,6 +210,20 @@ def test_cache_rejects_bad_tensors(rec, bad):
         fake_cache(**bad)
 
 
+@pytest.mark.parametrize("name", ["k_codes", "v_codes", "k_scale", "v_scale", "page_table", "weight", "pos", "B", "max_pages", "c"])
+def test_cache_keeps_the_tensors_it_was_made_with(rec, name):
+    """Calls use the addresses taken when the cache was made: another tensor in an attribute would free the one they point at."""
+    c, other = fake_cache(), fake_cache()
+    was = getattr(c, name)
+    with pytest.raises(AttributeError, match=name):
+        setattr(c, name, getattr(other, name))
+    with pytest.raises(AttributeError, match=name):
+        delattr(c, name)
+    with pytest.raises(AttributeError):
+        c.anything_else = 1
+    assert getattr(c, name) is was
+
+
 def test_calls_reject_bad_tensors(rec):
     c = fake_cache()
     kv = FakeCuda((2, 3, 2, 128), torch.bfloat16)
