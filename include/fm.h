@@ -412,7 +412,8 @@ size_t fm_cache_evict_workspace_bytes(const fm_kv_cache* src, int32_t budget);
  * new_len[b] = min(len[b], budget).  (A kept slot whose dst page is not there leaves its weight and pos only.)
  *   src, dst  same B, H_kv, D, code_type; src->weight is needed; dst may lie in the same pools
  *             as src, with a table of other pages: a page of dst must not be a page of src that is in
- *             use.  dst->weight and dst->pos may be NULL; src->pos NULL = the slot index.
+ *             use.  dst->weight and dst->pos may be NULL and share no word with src's; src->pos NULL =
+ *             the slot index.
  *   len       device int32 [B]; new_len device int32 [B] (may be len itself)
  *   budget    1 <= budget <= 64 * dst->max_pages; 0 <= recent <= budget
  *   ws        device workspace, 256-byte aligned; calls that may overlap on the GPU need one each

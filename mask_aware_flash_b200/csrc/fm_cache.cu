@@ -661,6 +661,14 @@ cudaError_t launch_select(const EvictParams& p, int B, int cluster, cudaStream_t
   return cudaLaunchKernelEx(&cfg, select_kernel<kHeld, kThreads>, p);
 }
 
+// Do two caches' tables of a word per slot (weight, pos) share any word?
+bool slot_words_overlap(const fm_kv_cache* a, const void* x, const fm_kv_cache* b, const void* y) {
+  if (!x || !y) return false;
+  const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), y0 = reinterpret_cast<uintptr_t>(y);
+  auto bytes = [](const fm_kv_cache* c) { return (uintptr_t)c->B * c->H_kv * c->max_pages * kPage * 4; };
+  return x0 < y0 + bytes(b) && y0 < x0 + bytes(a);
+}
+
 size_t evict_n_kept_offset(const fm_kv_cache* src, int32_t budget) {
   return ((size_t)src->B * src->H_kv * budget * 4 + 255) / 256 * 256;
 }
@@ -718,7 +726,9 @@ fm_status fm_cache_evict(const fm_kv_cache* src, const fm_kv_cache* dst, const i
   if (src->page_table == dst->page_table && src->k_codes == dst->k_codes) return FM_ERR_INVALID_ARG;
   if (!src->weight || !len || !new_len) return FM_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(len) | reinterpret_cast<uintptr_t>(new_len)) & 3) return FM_ERR_INVALID_ARG;
-  if (dst->weight == src->weight || (dst->pos && dst->pos == src->pos)) return FM_ERR_INVALID_ARG;
+  if (fm::slot_words_overlap(src, src->weight, dst, dst->weight) || fm::slot_words_overlap(src, src->weight, dst, dst->pos) ||
+      fm::slot_words_overlap(src, src->pos, dst, dst->weight) || fm::slot_words_overlap(src, src->pos, dst, dst->pos))
+    return FM_ERR_INVALID_ARG;
   if (budget < 1 || budget > (int64_t)dst->max_pages * fm::kPage || recent < 0 || recent > budget)
     return FM_ERR_INVALID_ARG;
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255) || ws_bytes < fm_cache_evict_workspace_bytes(src, budget))

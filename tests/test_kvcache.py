@@ -133,6 +133,22 @@ def test_evict_refusals(L):
     assert f(nbytes=n - 1) == fm.FM_ERR_WORKSPACE
 
 
+def test_evict_refuses_overlapping_weights_and_positions(L):
+    """Another cache's weight or pos that shares some of its words: slots would be read after others were written."""
+    r = ctypes.byref
+    src = cache_c(weight=0x200000, pos=0x300000)    # 2 x 2 x 256 words: 0x1000 bytes each
+    far = dict(page_table=0x150000, weight=0x400000, pos=0x500000, max_pages=2)  # 0x800 bytes each
+
+    def f(**kw):  # (without a workspace: FM_ERR_WORKSPACE where the caches are accepted, and never a launch)
+        return L.fm_cache_evict(r(src), r(cache_c(**dict(far, **kw))), 0x600000, 100, 10, 0x610000, None, 0, None)
+    assert f() == fm.FM_ERR_WORKSPACE and f(weight=None, pos=None) == fm.FM_ERR_WORKSPACE
+    for name, other in (("weight", 0x200000), ("pos", 0x300000), ("weight", 0x300000), ("pos", 0x200000)):
+        for at in (other, other + 4, other + 0xFFC, other - 0x7FC):
+            assert f(**{name: at}) == fm.FM_ERR_INVALID_ARG, (name, hex(at))
+        for at in (other + 0x1000, other - 0x800):  # side by side
+            assert f(**{name: at}) == fm.FM_ERR_WORKSPACE, (name, hex(at))
+
+
 def key_weight_args(**kw):
     d = dict(B=1, H=4, n_q=256, n_k=256, D=128, dtype=0, scale=0.1, q=0x10000, k=0x20000, H_kv=2)
     d.update(kw)
