@@ -172,6 +172,35 @@ def test_append_float32_input(fm):
     np.testing.assert_array_equal(got, c.ref.units["v"][1, :, 1])
 
 
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_append_float32_values_and_runs(fm, D, code):
+    """fp32 tokens of every kind: numbers that no bf16 holds, the largest and the subnormal ones, infinities and NaN, runs over
+    pages' ends and single tokens into open blocks whose scale grows."""
+    B, H_kv, max_pages = 2, 2, 5
+    r = np.random.default_rng(D + 7)
+    c = Pair(fm, B, H_kv, D, max_pages, code, seed=D)
+    lens = np.array([0, 50])
+    for scale in (c.t.k_scale, c.t.v_scale):  # sequence 1 begins behind 50 slots of zeros
+        scale.zero_()
+    c.ref.weight[1, :, :50], c.ref.pos[1, :, :50] = 3.0, -5
+    first = True
+    for n_new in (200, 1, 1, 30):
+        k, v = (x.astype(np.float32) for x in tokens(r, B, n_new, H_kv, D, spread=4.0))
+        if first:
+            k[0, :64] *= np.float32(2.0 ** -140)   # a block of subnormal numbers
+            k[0, 64, 0, :5] = [np.inf, -np.inf, np.nan, 3.4028235e38, -1e-45]
+            v[0, 130:192] = np.nan
+            v[1, 3, 1, 7] = 1e38
+        first = False
+        start = lens.copy()
+        fm.fm_cache_append(c.t, torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), i32(start), row=i32(start + 3))
+        c.ref.append(k.astype(np.float64), v.astype(np.float64), start, row=start + 3)
+        lens = lens + n_new
+        c.check(lens)
+    assert fm.fm_get_device_status() == 0
+
+
 # --------------------------------------------------------------------------------------------- attention
 def mask_vectors(kind, n, B, Hm, r):
     """Four int32 arrays [B, Hm, n] (or None each)."""
