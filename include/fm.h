@@ -313,7 +313,8 @@ fm_status fm_attn_bwd_noalloc(const fm_attn_args* a, const fm_mask_meta* meta, c
  *   Scale rule: with amax the largest finite |x| of the block and Qmax 127 (int8) or 448 (e4m3), the
  *   scale is 0 if amax = 0, else the smallest power of two 2^e >= amax / Qmax, e >= -126; codes are
  *   x / scale rounded to nearest, ties to even, after clamping to [-Qmax, Qmax] (so infinities
- *   saturate); NaN becomes 0.  Powers of two make the division exact, so a code has one rounding.
+ *   saturate, to 0 where the block's finite values are all 0); NaN becomes 0.  Powers of two make the
+ *   division exact, so a code has one rounding.
  *   D is 64, 128 or 256; n_pages * H_kv * 64 is below 2^31, B * H_kv * max_pages * 64 below 2^30; B, H_kv <= 65535.
  */
 typedef struct {
@@ -368,9 +369,10 @@ size_t fm_cache_attn_workspace_bytes(const fm_kv_cache* cache, const fm_cache_at
 /*
  * For every sequence b, query t and head h, with U the unmasked keys among the first len[b] slots of
  * K/V head h / (H / H_kv):  O = sum_{j in U} softmax_j(scale q.k_j) v_j and
- * LSE = ln sum_{j in U} exp(scale q.k_j); U empty: O = 0, LSE = -inf (as fm_attn_fwd).  The scores have
- * to lie in fp32's range.  A key's share of O counts as 0 where its softmax weight is under 2^-110, and
- * may lose bits where it is under 2^-100 of the row's largest element of O.  Blocks whose
+ * LSE = ln sum_{j in U} exp(scale q.k_j); U empty: O = 0, LSE = -inf (as fm_attn_fwd).  A row's largest
+ * |q| times scale times a block's largest |k| has to lie in fp32's range.  A key's share of O counts as
+ * 0 where its softmax weight is under 2^-110, and may lose bits where it is under 2^-100 of the row's
+ * largest element of O.  Blocks whose
  * keys are masked for every row are not read.  accumulate = 1: weight[b, hk, j] += the sum of key j's
  * softmax weights over the rows of the heads that share hk.  Every sum has a fixed order: the same
  * call gives the same bits.

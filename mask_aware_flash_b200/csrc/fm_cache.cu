@@ -773,7 +773,7 @@ fm_status fm_cache_evict(const fm_kv_cache* src, const fm_kv_cache* dst, const i
   p.chunk = (int)(((slots + cluster - 1) / cluster + 31) / 32 * 32);
   const bool held = p.chunk <= fm::kSelMaxKeys;
   // 1024 threads a CTA where there is one CTA per SM at most (2 x 8 heads of 40000 slots: 24 us, with 512 threads 28), 512
-  // where two share one (32 x 8 heads of 4200: 70 us, with 1024 threads 72)
+  // where two share one (32 x 8 heads of 4200: 62.0 us, with 1024 threads 63.2)
   const bool wide = lists * cluster <= 148;
   cudaError_t e = held ? (wide ? fm::launch_select<true, 1024>(p, src->B, cluster, s) : fm::launch_select<true, 512>(p, src->B, cluster, s))
                        : fm::launch_select<false, 1024>(p, src->B, cluster, s);

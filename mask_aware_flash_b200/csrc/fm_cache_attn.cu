@@ -21,10 +21,9 @@
 // product of q and the cached key, summed in fp32.  The contraction orders are permuted so that a thread's
 // operands are 16 consecutive bytes of a row: over d for K; for V by pairing the bytes of two tokens.
 //
-// Device time (graph of back-to-back calls; D = 128, 8 K/V heads of 4 query heads): one sequence of 131072 tokens 53 us, 5.1 TB/s
+// Device time (graph of back-to-back calls; D = 128, 8 K/V heads of 4 query heads): one sequence of 131072 tokens 52 us, 5.2 TB/s
 // of codes, of which some 8 us are the start (launch, dependent loads, first copies) and the join; 64 ragged ones of up to 8192
-// with weights 146 us, of which the scores' write and the weights' pass are some 35.  One of 517 tokens (D = 64): 9.8 us, all of
-// it latency.
+// (e4m3) with weights 146 us, without 122.  One of 517 tokens (D = 64): 9.5 us, all of it latency.
 #include "fm_cache.cuh"
 
 namespace fm {
@@ -42,7 +41,7 @@ constexpr float kPBias = 14.f;
 // lost where V's scales or the softmax weights of two blocks are far apart, in either order, and a block that a row does not see does
 // not matter to it.  O moves with u, in fp32, as far as 2^kORoom; so what a block adds loses bits only where it is under 2^-118 of the
 // largest element of the row's O.  (One unit for all rows, the block's scale, loses rows whose scales are 2^80 under another row's; a
-// unit per row costs 1% at 8 rows, 4% at 32 rows of D = 64: 32 sequences of 8192 tokens 74.6 -> 77.5 us.)
+// unit per row costs up to 1% at 8 rows, 3% at 32 rows of D = 64: 32 sequences of 8192 tokens 74.2 -> 76.4 us.)
 constexpr float kPMid = 7.75f;  // half of 15.5
 constexpr int kORoom = 118, kUnitMax = 126;
 
@@ -1004,7 +1003,7 @@ __global__ void __launch_bounds__(kJoinThreads, kWeightSlots == 512 ? 8 : 6) cac
     if (threadIdx.x == 0) p.lse[((int64_t)b * p.H + h) * p.n_q + tq] = t.y == 0.f ? kNegInf : (t.x + log2f(t.y)) * kLn2;
     return;
   }
-  // Weights.  Four keys a thread; what does not depend on anything is loaded first, so that there are two memory latencies
+  // Weights.  kWeightSlots / kJoinThreads keys a thread; what does not depend on anything is loaded first, so that there are two memory latencies
   // on the way, not one for each of length, runs, sums, liveness, scores.
   constexpr int kKeys = kWeightSlots / kJoinThreads;
   const int cap = p.max_pages * kPage, per_bh = (cap + kWeightSlots - 1) / kWeightSlots;
@@ -1062,8 +1061,8 @@ __global__ void __launch_bounds__(kJoinThreads, kWeightSlots == 512 ? 8 : 6) cac
 
 // ------------------------------------------------------------------------------------------- host
 // Tiles of 8 query rows that a CTA holds.  More than one spares reading (through L2) and decoding the cache again for the next
-// rows, as far as the accumulators fit the registers: 32 sequences of 8192 tokens, 4 K/V heads, D = 128, 16 rows: 69 us with two
-// tiles, 90 with one; D = 64, 32 rows: 78 us with four, 86 with two, 126 with one.  At D = 256 two tiles leave room for half the
+// rows, as far as the accumulators fit the registers: 32 sequences of 8192 tokens, 4 K/V heads, D = 128, 16 rows: 66 us with two
+// tiles, 89 with one; D = 64, 32 rows: 76 us with four, 88 with two, 125 with one.  At D = 256 two tiles leave room for half the
 // warps, which costs what they spare (16 rows: 92 us either way).  Where the table is so small that the rows' CTAs all
 // end after one turn of their warps, a tile each: 500 tokens, 8 K/V heads, D = 128, 16 rows: 10.8 us against 12.3; D = 64, 32
 // rows: 9.8 against 13.4.

@@ -10,8 +10,8 @@
 // copies and products of the next key tile start while the last one is still being summed.  Where there are too few
 // key tiles for the SMs a cluster of CTAs shares each one's query tiles and adds up through distributed shared memory.
 // Bound by the exponentials: per score there is one against 2 D flops of the tensor core, and for D = 128 the MUFU unit takes 1024
-// clocks for a tile's 16384 (16 a clock) against 512 of the product.  8192 tokens in documents, 16 heads, D = 128: 51 us, 7888
-// tiles, 0.59 of that rate; the rest are a tile's other instructions (TMEM loads, multiply-adds and additions share the issue
+// clocks for a tile's 16384 (16 a clock) against 512 of the product.  8192 tokens in documents, 16 heads, D = 128: 50 us, 7888
+// tiles, 0.56 of that rate at 1965 MHz; the rest are a tile's other instructions (TMEM loads, multiply-adds and additions share the issue
 // slots with them: without the exponentials it takes 37 us, without the products too 25) and the ends of 1024 uneven lists.
 // 2 x 3996 tokens, 16 heads, D = 64: 53 us, the same unit.  1024 tokens, 8 heads: 13 us, latency (launch, lists, one or two tiles
 // a warpgroup, the cluster's sum).
@@ -136,7 +136,9 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) { 
 
 // Adds the weights of 32 scores to the four running sums; bit i of `masked` (only of a partial tile): query i does not see
 // the key.  nl: -LSE of the queries in log2 units.  (One score an instruction: packed pairs would halve the multiply-adds and
-// additions, but cost more register moves than that.)
+// additions, but cost more register moves than that.)  Scale and LSE come in log2 units, rounded to fp32 first: a weight is off by a
+// few 2^-24 of |s| + |LSE| and by the exponential's 2^-22 (the weights by 1.3e-7 to 1.9e-7 of their norm, an fp32 form with an exact
+// exponential by 0.6e-7).
 __device__ __forceinline__ void add_block(const uint32_t (&s)[32], const float* nl, float scale, bool partial, uint32_t masked,
                                           float (&acc)[4]) {
   float w[32];
