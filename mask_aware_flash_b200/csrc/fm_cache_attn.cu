@@ -892,12 +892,12 @@ __global__ void __launch_bounds__(CacheAttnCfg<D, NT>::kThreads, 1)
 
 // Last kernel (it may be resident before the one before ends, so what that wrote is read through L2).  The first CTAs join
 // the rows of the (sequence, head)s that several runs share, a CTA per row: with M the largest of the runs' maxima,
-// l = sum_c l_c 2^(m_c - M), O = sum_c O_c (l_c 2^(m_c - M) / l), O_c the run's own quotient (of a value's size, so no sum overflows).  The others add the softmax weights 2^(s - M) / l of kWeightSlots keys
-// each to the cache's, from the stored scores: 4 bytes per key and row written and read (for 4 rows 32 bytes beside a key's 256 of codes), against
-// reading K again and forming its products twice.  1024 slots a CTA, 8 a thread, for up
-// to 8 rows: 64 ragged sequences of up to 8192 tokens, 8 K/V heads, 4 rows: 145 us for the call (five CTAs an SM instead of six:
-// 148); 512 slots: 150; 2048: 4 sequences
-// of 2048 take 15.0 us instead of 13.7.  512 slots and more CTAs on an SM beyond, where a CTA's time is its rows': 21 sequences of
+// l = sum_c l_c 2^(m_c - M), O = sum_c O_c (l_c 2^(m_c - M) / l), O_c the run's own quotient (of a value's size, so no sum
+// overflows).  The others add the softmax weights 2^(s - M) / l of kWeightSlots keys each to the cache's, from the stored scores:
+// 4 bytes per key and row written and read (for 4 rows 32 bytes beside a key's 256 of codes), against reading K again and forming
+// its products twice.  1024 slots a CTA, 8 a thread, for up to 8 rows: 64 ragged sequences of up to 8192 tokens, 8 K/V heads, 4
+// rows: 145 us for the call (five CTAs an SM instead of six: 148); 512 slots: 150; 2048: 4 sequences of 2048 take 15.0 us instead
+// of 13.7.  512 slots and more CTAs on an SM beyond, where a CTA's time is its rows': 21 sequences of
 // up to 19055 tokens, 80 rows: 305 us; with 1024 slots 347.
 constexpr int kJoinThreads = 128;
 constexpr int weight_slots(int n_rows) { return n_rows <= 8 ? 1024 : 512; }
